@@ -19,6 +19,8 @@ enum : int {
   DEV_ERR_TIMEOUT_ATTN = 4,       // attention pipeline wait ran out
   DEV_ERR_BAD_INDEX = 5,          // an id or index outside its range was seen and skipped
   DEV_ERR_TIMEOUT_ROUTE = 6,      // a top-k CTA waited too long for the expert offsets of its launch
+  DEV_ERR_NO_PAGES = 7,           // a cache has too few free pages for a call (nothing was changed)
+  DEV_ERR_BAD_COUNT = 8,          // a row count or a growth that does not fit its sequence (skipped)
 };
 
 // Every spin-wait gives up after this many nanoseconds of %globaltimer and reports an error.

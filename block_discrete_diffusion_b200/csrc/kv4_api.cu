@@ -1,0 +1,253 @@
+// kv4_api.cu -- entry points of the paged 4-bit cache (include/dg.h): argument checks and launches.  Host code only.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "dg.h"
+#include "kv4_kernels.h"
+
+#define DG_API extern "C" __attribute__((visibility("default")))
+
+using namespace dg;
+
+namespace {
+
+dg_status bad(const char* fn, const char* why, dg_status st = DG_ERR_INVALID_ARG) {
+  char msg[256];
+  snprintf(msg, sizeof msg, "%s: %s", fn, why);
+  return record_error(st, msg);
+}
+
+dg_status launched(const char* fn, cudaError_t e) {
+  return e == cudaSuccess ? DG_OK : bad(fn, cudaGetErrorString(e), DG_ERR_CUDA);
+}
+
+constexpr int kMaxPages = 1 << 24;
+
+const char* shape_error(const dg_kv4_cache* c) {
+  if (!c) return "null cache";
+  if (c->d_head != 64 && c->d_head != 128) return "d_head must be 64 or 128";
+  if (c->n_layers <= 0 || c->n_kv <= 0 || c->n_pages <= 0 || c->n_seq <= 0 || c->max_pages <= 0)
+    return "sizes must be positive";
+  if (c->n_seq > 4096) return "n_seq must be at most 4096";
+  if (c->n_pages > kMaxPages || c->max_pages > kMaxPages) return "n_pages and max_pages must be at most 2^24";
+  if ((long long)c->n_seq * c->max_pages >= 1ll << 30) return "n_seq * max_pages must be below 2^30";
+  if ((long long)c->n_seq * c->n_kv > 65535) return "n_seq * n_kv must be at most 65535";
+  return nullptr;
+}
+
+size_t pad4(size_t n) { return (n + 3) & ~size_t(3); }
+
+size_t pool_bytes(const dg_kv4_cache* c) {
+  return (size_t)c->n_layers * c->n_pages * c->n_kv * 72 * c->d_head;
+}
+size_t table_words(const dg_kv4_cache* c) { return pad4((size_t)c->n_seq * c->max_pages); }
+size_t book_words(const dg_kv4_cache* c) {
+  return KV4_HEAD_WORDS + pad4(c->n_seq) + 4 * pad4(c->n_pages) + table_words(c);
+}
+
+bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+dg_status check_cache(const char* fn, const dg_kv4_cache* c) {
+  if (const char* why = shape_error(c)) return bad(fn, why);
+  if (!aligned16(c->d_pool) || !aligned16(c->d_book)) return bad(fn, "pool and book must be 16-byte aligned device buffers");
+  if (c->pool_bytes < pool_bytes(c)) return bad(fn, "pool too small", DG_ERR_CAPACITY);
+  if (c->book_bytes < 4 * book_words(c)) return bad(fn, "book too small", DG_ERR_CAPACITY);
+  return DG_OK;
+}
+
+Kv4View view(const dg_kv4_cache* c) {
+  Kv4View v{};
+  int32_t* w = static_cast<int32_t*>(c->d_book);
+  auto take = [&](size_t words) {
+    int32_t* p = w;
+    w += words;
+    return p;
+  };
+  v.pool = static_cast<uint8_t*>(c->d_pool);
+  v.head = take(KV4_HEAD_WORDS);
+  v.lens = take(pad4(c->n_seq));
+  v.refs = take(pad4(c->n_pages));
+  v.table = take(table_words(c));
+  v.move_src = take(pad4(c->n_pages));
+  v.move_dst = take(pad4(c->n_pages));
+  v.map = take(pad4(c->n_pages));
+  v.n_layers = c->n_layers;
+  v.n_kv = c->n_kv;
+  v.dh = c->d_head;
+  v.n_pages = c->n_pages;
+  v.n_seq = c->n_seq;
+  v.max_pages = c->max_pages;
+  return v;
+}
+
+int current_sms() {
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  return n;
+}
+
+// Key splits of the few-rows form: enough CTAs to fill the SMs once, at least one page for each of a CTA's warps.
+constexpr int kMaxSplits = 64;
+int few_splits(const dg_kv4_cache* c, int n_q, int rows, long long plan_len) {
+  const long long tiles = ((long long)rows * (n_q / c->n_kv) + kKv4FewRows - 1) / kKv4FewRows;
+  const long long units = tiles * c->n_seq * c->n_kv;
+  const long long slots = (long long)current_sms() * (c->d_head == 128 ? 2 : 4);
+  const long long pages = (plan_len + DG_KV4_PAGE - 1) / DG_KV4_PAGE;
+  return (int)std::max(1ll, std::min({(long long)kMaxSplits, slots / units, (pages + 3) / 4}));
+}
+
+dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_kv4_rows* r) {
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!r || !aligned16(r->k) || !aligned16(r->v)) return bad(fn, "k and v must be 16-byte aligned device buffers");
+  if (layer < 0 || layer >= c->n_layers) return bad(fn, "layer out of range");
+  if (r->dtype != DG_DTYPE_BF16 && r->dtype != DG_DTYPE_FP16) return bad(fn, "dtype must be bf16 or fp16");
+  if (r->rows <= 0) return bad(fn, "rows must be positive");
+  if ((r->k_seq | r->k_row | r->k_head | r->v_seq | r->v_row | r->v_head) & 7)
+    return bad(fn, "strides must be multiples of 8 elements");
+  return DG_OK;
+}
+
+Kv4Rows rows_of(const dg_kv4_rows* r) {
+  return Kv4Rows{r->k, r->v, r->k_seq, r->k_row, r->k_head, r->v_seq, r->v_row, r->v_head, r->d_rows, r->rows,
+                 r->dtype == DG_DTYPE_FP16};
+}
+
+}  // namespace
+
+DG_API size_t dg_kv4_pool_bytes(const dg_kv4_cache* c) { return shape_error(c) ? 0 : pool_bytes(c); }
+DG_API size_t dg_kv4_book_bytes(const dg_kv4_cache* c) { return shape_error(c) ? 0 : 4 * book_words(c); }
+
+DG_API dg_status dg_kv4_init(const dg_kv4_cache* c, void* stream) {
+  const char* fn = "dg_kv4_init";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  const Kv4View v = view(c);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(c->d_book, 0, 4 * book_words(c), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(v.table, 0xff, 4 * table_words(c), s);
+  return launched(fn, e);
+}
+
+DG_API dg_status dg_kv4_extend(const dg_kv4_cache* c, const int32_t* d_counts, void* stream) {
+  const char* fn = "dg_kv4_extend";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!d_counts) return bad(fn, "counts are null");
+  return launched(fn, kv4_extend(view(c), d_counts, current_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+DG_API dg_status dg_kv4_fork(const dg_kv4_cache* c, const int32_t* d_src, const int32_t* d_dst, int n, void* stream) {
+  const char* fn = "dg_kv4_fork";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!d_src || !d_dst) return bad(fn, "src or dst is null");
+  if (n <= 0 || n > c->n_seq) return bad(fn, "n must be in [1, n_seq]");
+  return launched(fn, kv4_fork(view(c), d_src, d_dst, n, static_cast<cudaStream_t>(stream)));
+}
+
+DG_API dg_status dg_kv4_free(const dg_kv4_cache* c, const int32_t* d_slots, int n, void* stream) {
+  const char* fn = "dg_kv4_free";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!d_slots) return bad(fn, "slots are null");
+  if (n <= 0 || n > c->n_seq) return bad(fn, "n must be in [1, n_seq]");
+  return launched(fn, kv4_free(view(c), d_slots, n, static_cast<cudaStream_t>(stream)));
+}
+
+DG_API dg_status dg_kv4_compact(const dg_kv4_cache* c, void* stream) {
+  const char* fn = "dg_kv4_compact";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  return launched(fn, kv4_compact(view(c), current_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+DG_API dg_status dg_kv4_append(const dg_kv4_cache* c, int layer, const dg_kv4_rows* r, void* stream) {
+  const char* fn = "dg_kv4_append";
+  const dg_status st = check_rows(fn, c, layer, r);
+  if (st != DG_OK) return st;
+  return launched(fn, kv4_rows(view(c), layer, rows_of(r), true, static_cast<cudaStream_t>(stream)));
+}
+
+DG_API dg_status dg_kv4_read(const dg_kv4_cache* c, int layer, const dg_kv4_rows* r, void* stream) {
+  const char* fn = "dg_kv4_read";
+  const dg_status st = check_rows(fn, c, layer, r);
+  if (st != DG_OK) return st;
+  return launched(fn, kv4_rows(view(c), layer, rows_of(r), false, static_cast<cudaStream_t>(stream)));
+}
+
+DG_API size_t dg_kv4_attend_workspace_bytes(const dg_kv4_cache* c, int n_q, int rows) {
+  if (shape_error(c) || n_q <= 0 || n_q % c->n_kv || rows <= 0) return 0;
+  const size_t splits = few_splits(c, n_q, rows, (long long)c->max_pages * DG_KV4_PAGE);
+  return splits * c->n_seq * rows * n_q * (4 * (size_t)c->d_head + 4) + 1024;
+}
+
+DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_attn* a, void* ws, size_t ws_bytes,
+                               void* stream) {
+  const char* fn = "dg_kv4_attend";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!a || !aligned16(a->q) || !aligned16(a->out)) return bad(fn, "q and out must be 16-byte aligned device buffers");
+  if (layer < 0 || layer >= c->n_layers) return bad(fn, "layer out of range");
+  if (a->dtype != DG_DTYPE_BF16 && a->dtype != DG_DTYPE_FP16) return bad(fn, "dtype must be bf16 or fp16");
+  if (a->n_q <= 0 || a->n_q % c->n_kv) return bad(fn, "n_q must be a positive multiple of n_kv");
+  if (a->rows <= 0 || a->rows > 65536) return bad(fn, "rows must be in [1, 65536]");
+  if (a->causal != 0 && a->causal != 1) return bad(fn, "causal must be 0 or 1");
+  if (!(a->scale > 0.f) || !isfinite(a->scale)) return bad(fn, "scale must be positive and finite");
+  if (a->plan_len < 0) return bad(fn, "plan_len must not be negative");
+  if ((a->q_seq | a->q_row | a->q_head | a->o_seq | a->o_row | a->o_head) & 7)
+    return bad(fn, "strides must be multiples of 8 elements");
+  if (!ws || ws_bytes < dg_kv4_attend_workspace_bytes(c, a->n_q, a->rows))
+    return bad(fn, "workspace too small", DG_ERR_CAPACITY);
+  const long long most = (long long)c->max_pages * DG_KV4_PAGE;
+  const long long plan = a->plan_len > 0 ? std::min<long long>(a->plan_len, most) : most;
+  Kv4Attn k{};
+  k.q = a->q;
+  k.out = a->out;
+  k.lse = a->lse;
+  k.n_rows = a->d_rows;
+  k.q_seq = a->q_seq;
+  k.q_row = a->q_row;
+  k.q_head = a->q_head;
+  k.o_seq = a->o_seq;
+  k.o_row = a->o_row;
+  k.o_head = a->o_head;
+  k.n_q = a->n_q;
+  k.rows = a->rows;
+  k.causal = a->causal;
+  k.fp16 = a->dtype == DG_DTYPE_FP16;
+  k.scale = a->scale;
+  k.n_splits = few_splits(c, a->n_q, a->rows, plan);
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
+  const size_t n = (size_t)k.n_splits * c->n_seq * a->rows * a->n_q;
+  k.part_o = base;
+  k.part_lse = reinterpret_cast<float*>(base + n * c->d_head * 4);
+  const Kv4View v = view(c);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = kv4_attend_few(v, layer, k, s);
+  if (e == cudaSuccess && k.n_splits > 1) e = kv4_attend_merge(v, k, true, s);
+  return launched(fn, e);
+}
+
+DG_API dg_status dg_kv4_error(const dg_kv4_cache* c, void* stream, int* h_code) {
+  const char* fn = "dg_kv4_error";
+  const dg_status st = check_cache(fn, c);
+  if (st != DG_OK) return st;
+  if (!h_code) return bad(fn, "h_code is null");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int32_t w[4] = {0, 0, 0, 0};
+  const Kv4View v = view(c);
+  cudaError_t e = cudaMemcpyAsync(w, v.head, sizeof w, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(v.head + KV4_WORD_ERR, 0, 4, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(v.head + KV4_WORD_WAIT, 0, 4, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return launched(fn, e);
+  *h_code = w[KV4_WORD_ERR] ? w[KV4_WORD_ERR] : w[KV4_WORD_WAIT];
+  if (!*h_code) return DG_OK;
+  char why[64];
+  snprintf(why, sizeof why, "device-side error code %d", *h_code);
+  return bad(fn, why, DG_ERR_DEVICE);
+}

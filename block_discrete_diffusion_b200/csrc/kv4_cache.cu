@@ -1,0 +1,563 @@
+// kv4_cache.cu -- the paged 4-bit cache: rows in and out, and its pages.
+//
+// Rows.  A CTA owns one (sequence, page, KV head) block, so every byte of a page has one writer.  A thread takes
+// whole words of the block (positions g and g + 8 of K, a quad of positions of V) with all 16 channels of a
+// scale: it needs no exchange with its neighbours, and only words that some other row shares are read first.
+// Bound by memory: a value costs 2 bytes on one side and 0.5625 on the other.
+//
+// Pages.  The book (lengths, reference counts, tables) is a few hundred KB at most and its updates depend on one
+// another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left
+// as a list of (from, to) for a second launch over the whole GPU.  Nothing changes when a call cannot be
+// carried out whole: the error word tells.
+#include "kv4.cuh"
+#include "kv4_kernels.h"
+
+namespace dg {
+
+bool first_on_device(unsigned long long* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return true;
+  const unsigned long long bit = 1ull << dev;
+  return !(__atomic_fetch_or(done, bit, __ATOMIC_RELAXED) & bit);
+}
+
+namespace {
+
+// 16 elements (32 bytes) of a row
+template <typename T>
+__device__ __forceinline__ void load16(const void* base, long long at, float (&x)[16]) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 q = p[i];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x[8 * i + 2 * c] = Half<T>::lo(w[c]);
+      x[8 * i + 2 * c + 1] = Half<T>::hi(w[c]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(void* base, long long at, const float (&x)[16]) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(base) + at);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    p[i] = make_uint4(Half<T>::pack(x[8 * i], x[8 * i + 1]), Half<T>::pack(x[8 * i + 2], x[8 * i + 3]),
+                      Half<T>::pack(x[8 * i + 4], x[8 * i + 5]), Half<T>::pack(x[8 * i + 6], x[8 * i + 7]));
+}
+
+// Scale byte of 16 values; the values become quotients on the grid that to_e2m1x2 rounds.
+__device__ __forceinline__ uint32_t to_quotients(float (&x)[16]) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+  const uint32_t byte = ue5m3_scale(amax);
+  const float s = ue5m3_to_f32(byte);
+  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = on_grid(x[i], r);
+  return byte;
+}
+
+__device__ __forceinline__ void merge_words(uint4* p, uint4 v, uint32_t mask) {
+  if (mask == 0xffffffffu) {
+    *p = v;
+    return;
+  }
+  const uint4 o = *p;
+  *p = make_uint4((o.x & ~mask) | (v.x & mask), (o.y & ~mask) | (v.y & mask), (o.z & ~mask) | (v.z & mask),
+                  (o.w & ~mask) | (v.w & mask));
+}
+
+constexpr int kRowThreads = 128;
+
+// Rows [len - n, len) of every sequence into (Write) or out of its pages.
+template <int DH, typename T, bool Write>
+__global__ void __launch_bounds__(kRowThreads) kv4_rows_kernel(Kv4View c, int layer, Kv4Rows r) {
+  using F = Kv4<DH>;
+  pdl_trigger();
+  pdl_wait();
+  const int seq = blockIdx.z, head = blockIdx.y;
+  const int len = c.lens[seq];
+  const int n = r.n_rows ? r.n_rows[seq] : r.rows;
+  if (n == 0) return;
+  const long long cap = (long long)c.max_pages * kPage;
+  if (n < 0 || n > r.rows || n > len || len > cap) {
+    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_COUNT);
+    return;
+  }
+  const int start = len - n;
+  const int lp = start / kPage + blockIdx.x;
+  if ((long long)lp * kPage >= len) return;
+  const int page = c.table[(size_t)seq * c.max_pages + lp];
+  if (page < 0 || page >= c.n_pages || (Write && c.refs[page] != 1)) {   // a shared page is nobody's to write
+    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+    return;
+  }
+  uint8_t* block = c.pool + (((size_t)layer * c.n_pages + page) * c.n_kv + head) * F::kBytes;
+  const int lo = max(start - lp * kPage, 0), hi = min(len - lp * kPage, kPage);   // positions of this page
+  const long long row0 = (long long)lp * kPage - start;                          // row of the page's position 0
+  const long long kb = seq * r.k_seq + head * r.k_head, vb = seq * r.v_seq + head * r.v_head;
+
+  // K: positions p and p + 8 of a tile, one block of 16 channels
+  for (int i = threadIdx.x; i < (kPage / 2) * (DH / 16); i += kRowThreads) {
+    const int b = i % (DH / 16), pair = i / (DH / 16);
+    const int kt = pair / 8, g = pair % 8, t = b / F::kH, jh = b % F::kH;
+    const int p0 = kt * 16 + g, p1 = p0 + 8;
+    const bool in0 = p0 >= lo && p0 < hi, in1 = p1 >= lo && p1 < hi;
+    if (!in0 && !in1) continue;
+    uint4* words = reinterpret_cast<uint4*>(block + ((kt * F::kH + jh) * 32 + g * 4 + t) * 16);
+    uint8_t* sc = block + F::kSk + (g * 4 + t) * 8 * F::kH + 2 * kt * F::kH + jh;   // position g; g + 8 is kH further
+    float x0[16], x1[16];
+    if (Write) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x0[e] = x1[e] = 0.f;
+      if (in0) load16<T>(r.k, kb + (row0 + p0) * r.k_row + b * 16, x0);
+      if (in1) load16<T>(r.k, kb + (row0 + p1) * r.k_row + b * 16, x1);
+      const uint32_t s0 = to_quotients(x0), s1 = to_quotients(x1);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = to_e2m1x2(x0[4 * j], x0[4 * j + 1]) | to_e2m1x2(x1[4 * j], x1[4 * j + 1]) << 8 |
+               to_e2m1x2(x0[4 * j + 2], x0[4 * j + 3]) << 16 | to_e2m1x2(x1[4 * j + 2], x1[4 * j + 3]) << 24;
+      merge_words(words, make_uint4(w[0], w[1], w[2], w[3]),
+                  (in0 ? 0x00ff00ffu : 0u) | (in1 ? 0xff00ff00u : 0u));
+      if (in0) sc[0] = (uint8_t)s0;
+      if (in1) sc[F::kH] = (uint8_t)s1;
+    } else {
+      const uint4 q = *words;
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const float s0 = ue5m3_to_f32(sc[0]), s1 = ue5m3_to_f32(sc[F::kH]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+        e2m1_to_f16(w[j], o);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x0[4 * j + 2 * e] = Half<__half>::lo(o[2 * e]) * s0;
+          x0[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e]) * s0;
+          x1[4 * j + 2 * e] = Half<__half>::lo(o[2 * e + 1]) * s1;
+          x1[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e + 1]) * s1;
+        }
+      }
+      if (in0) store16<T>(r.k, kb + (row0 + p0) * r.k_row + b * 16, x0);
+      if (in1) store16<T>(r.k, kb + (row0 + p1) * r.k_row + b * 16, x1);
+    }
+  }
+
+  // V: positions 2t, 2t + 1, 2t + 8, 2t + 9 of a tile, one block of 16 channels
+  for (int i = threadIdx.x; i < 16 * (DH / 16); i += kRowThreads) {
+    const int b = i % (DH / 16), quad = i / (DH / 16);
+    const int kt = quad / 4, t = quad % 4;
+    const int p0 = kt * 16 + 2 * t;
+    bool in[4];
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = p0 + (e & 1) + 8 * (e >> 1);
+      in[e] = p >= lo && p < hi;
+      mask |= in[e] ? 0x0f0fu << (16 * (e >> 1) + 4 * (e & 1)) : 0u;
+    }
+    if (!mask) continue;
+    // channels 8 u .. 8 u + 7 of the block: the words of one (h, lane)
+    uint4* words[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int jh = F::kH == 2 ? u : 0, g = F::kH == 2 ? b : 2 * b + u;
+      words[u] = reinterpret_cast<uint4*>(block + F::kV + ((kt * F::kH + jh) * 32 + g * 4 + t) * 16);
+    }
+    uint32_t* sc = reinterpret_cast<uint32_t*>(block + F::kSv + ((b * 4 + t) * 4 + kt) * 4);
+    float x[4][16];
+    if (Write) {
+      uint32_t s = 0, smask = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[e][k] = 0.f;
+        if (in[e]) load16<T>(r.v, vb + (row0 + p0 + (e & 1) + 8 * (e >> 1)) * r.v_row + b * 16, x[e]);
+        s |= to_quotients(x[e]) << (8 * e);
+        smask |= in[e] ? 0xffu << (8 * e) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = 8 * u + 2 * j;
+          w[j] = to_e2m1x2(x[0][k], x[1][k]) | to_e2m1x2(x[0][k + 1], x[1][k + 1]) << 8 |
+                 to_e2m1x2(x[2][k], x[3][k]) << 16 | to_e2m1x2(x[2][k + 1], x[3][k + 1]) << 24;
+        }
+        merge_words(words[u], make_uint4(w[0], w[1], w[2], w[3]), mask);
+      }
+      *sc = smask == 0xffffffffu ? s : (*sc & ~smask) | (s & smask);
+    } else {
+      float s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = ue5m3_to_f32((*sc >> (8 * e)) & 0xff);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 q = *words[u];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t o[4];
+          e2m1_to_f16(w[j], o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {   // o[e]: channel e & 1, positions 2 (e >> 1) + {0, 1} of the quad
+            x[2 * (e >> 1)][8 * u + 2 * j + (e & 1)] = Half<__half>::lo(o[e]) * s[2 * (e >> 1)];
+            x[2 * (e >> 1) + 1][8 * u + 2 * j + (e & 1)] = Half<__half>::hi(o[e]) * s[2 * (e >> 1) + 1];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in[e]) store16<T>(r.v, vb + (row0 + p0 + (e & 1) + 8 * (e >> 1)) * r.v_row + b * 16, x[e]);
+    }
+  }
+}
+
+template <int DH, typename T>
+cudaError_t launch_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st) {
+  const int pages = (int)(((long long)r.rows + kPage - 2) / kPage + 1);   // the rows may begin at a page's last position
+  const dim3 grid(pages < c.max_pages ? pages : c.max_pages, c.n_kv, c.n_seq);
+  return launch_k(write ? kv4_rows_kernel<DH, T, true> : kv4_rows_kernel<DH, T, false>, grid, dim3(kRowThreads), 0, st,
+                  1, c, layer, r);
+}
+
+// ---------------------------------------------------------------------------------------------
+// the book
+// ---------------------------------------------------------------------------------------------
+constexpr int kBookThreads = 1024;
+constexpr int kMaxSeq = 4096;     // sequences of a cache (dg_kv4_cache): one word of shared memory each
+
+// exclusive prefix sum over the CTA's threads; *total: the sum (all threads)
+__device__ int block_scan(int v, int* total) {
+  __shared__ int warp_sums[33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += u;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = warp_sums[lane];
+    int ws = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, ws, o);
+      if (lane >= o) ws += u;
+    }
+    warp_sums[lane] = ws - w;
+    if (lane == 31) warp_sums[32] = ws;
+  }
+  __syncthreads();
+  const int before = warp_sums[warp] + s - v;
+  *total = warp_sums[32];
+  __syncthreads();
+  return before;
+}
+
+__device__ __forceinline__ int pages_of(long long len) { return (int)((len + kPage - 1) / kPage); }
+
+// What a sequence needs to grow by `count`: pages it has, whether it copies its last one, pages to take.
+struct Growth {
+  int have, copy, need, last;
+  bool bad;
+};
+__device__ Growth growth(const Kv4View& c, const int32_t* counts, int seq) {
+  Growth g{0, 0, 0, -1, false};
+  const int len = c.lens[seq], n = counts[seq];
+  const long long now = (long long)len + n;
+  if (n < 0 || len < 0 || now > (long long)c.max_pages * kPage) {
+    g.bad = true;
+    return g;
+  }
+  g.have = pages_of(len);
+  if (n > 0 && len % kPage) {
+    g.last = c.table[(size_t)seq * c.max_pages + g.have - 1];
+    if (g.last < 0 || g.last >= c.n_pages) {
+      g.bad = true;
+      return g;
+    }
+    g.copy = c.refs[g.last] > 1;
+  }
+  g.need = g.copy + pages_of(now) - g.have;
+  return g;
+}
+
+__global__ void __launch_bounds__(kBookThreads) kv4_extend_kernel(Kv4View c, const int32_t* counts) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int first[kMaxSeq + 1];   // index of a sequence's first page among the pages taken
+  __shared__ int bad, n_moves, n_free;
+  if (threadIdx.x == 0) bad = n_moves = n_free = 0;
+  __syncthreads();
+  // thread i: sequences [i per, i per + per), in order
+  const int per = (c.n_seq + kBookThreads - 1) / kBookThreads;
+  int mine = 0;
+  for (int s = threadIdx.x * per; s < min(c.n_seq, (int)(threadIdx.x + 1) * per); ++s) {
+    const Growth g = growth(c, counts, s);
+    if (g.bad) bad = 1;
+    mine += g.need;
+  }
+  int total;
+  int at = block_scan(mine, &total);
+  for (int s = threadIdx.x * per; s < min(c.n_seq, (int)(threadIdx.x + 1) * per); ++s) {
+    first[s] = at;
+    at += growth(c, counts, s).need;
+  }
+  if (threadIdx.x == 0) first[c.n_seq] = total;
+  __syncthreads();
+  if (bad) {
+    if (threadIdx.x == 0) {
+      report_error(c.head, DEV_ERR_BAD_COUNT);
+      c.head[KV4_WORD_MOVES] = 0;
+    }
+    return;
+  }
+  // the `total` lowest free pages (into c.map), 4 counts a thread at a time
+  for (int base = 0; base < c.n_pages && n_free < total; base += 4 * kBookThreads) {
+    const int p = base + 4 * threadIdx.x;
+    int v[4], k = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = p + e < c.n_pages && c.refs[p + e] == 0;
+      k += v[e];
+    }
+    int found;
+    int rank = n_free + block_scan(k, &found);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v[e]) {
+        if (rank < total) c.map[rank] = p + e;
+        ++rank;
+      }
+    if (threadIdx.x == 0) n_free += found;
+    __syncthreads();
+  }
+  if (n_free < total) {
+    if (threadIdx.x == 0) {
+      report_error(c.head, DEV_ERR_NO_PAGES);
+      c.head[KV4_WORD_MOVES] = 0;
+    }
+    return;
+  }
+  for (int i = threadIdx.x; i < total; i += kBookThreads) {
+    int lo = 0, hi = c.n_seq - 1;   // the last sequence whose first page is at or before i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (first[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int len = c.lens[lo], k = i - first[lo];
+    const int have = pages_of(len);
+    const int copy = first[lo + 1] - first[lo] - (pages_of((long long)len + counts[lo]) - have);
+    const int page = c.map[i];
+    int32_t* entry = c.table + (size_t)lo * c.max_pages + have - copy + k;
+    if (k < copy) {
+      const int m = atomicAdd(&n_moves, 1);
+      c.move_src[m] = *entry;
+      c.move_dst[m] = page;
+      atomicSub(c.refs + *entry, 1);
+    }
+    *entry = page;
+    c.refs[page] = 1;
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < c.n_seq; s += kBookThreads) c.lens[s] += counts[s];
+  if (threadIdx.x == 0) c.head[KV4_WORD_MOVES] = n_moves;
+}
+
+// Sequences dst[i] become second owners of src[i]'s pages, one warp for each pair.
+__global__ void __launch_bounds__(kBookThreads) kv4_fork_kernel(Kv4View c, const int32_t* src, const int32_t* dst, int n) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int times[kMaxSeq];   // how often a sequence is a destination
+  __shared__ int bad;
+  for (int s = threadIdx.x; s < c.n_seq; s += kBookThreads) times[s] = 0;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBookThreads) {
+    const int a = src[i], b = dst[i];
+    if (a < 0 || a >= c.n_seq || b < 0 || b >= c.n_seq || c.lens[b] != 0 || c.lens[a] < 0 ||
+        (long long)c.lens[a] > (long long)c.max_pages * kPage)
+      bad = 1;
+    else
+      atomicAdd(times + b, 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n && !bad; i += kBookThreads)
+    if (times[dst[i]] != 1 || times[src[i]] != 0) bad = 1;
+  __syncthreads();
+  if (bad) {
+    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += kBookThreads / 32) {
+    const int a = src[i], b = dst[i], len = c.lens[a];
+    for (int k = lane; k < pages_of(len); k += 32) {
+      const int page = c.table[(size_t)a * c.max_pages + k];
+      c.table[(size_t)b * c.max_pages + k] = page;
+      if (page >= 0 && page < c.n_pages) atomicAdd(c.refs + page, 1);
+    }
+    if (lane == 0) c.lens[b] = len;
+  }
+}
+
+__global__ void __launch_bounds__(kBookThreads) kv4_free_kernel(Kv4View c, const int32_t* slots, int n) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ int times[kMaxSeq];
+  __shared__ int bad;
+  for (int s = threadIdx.x; s < c.n_seq; s += kBookThreads) times[s] = 0;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBookThreads) {
+    const int s = slots[i];
+    if (s < 0 || s >= c.n_seq)
+      bad = 1;
+    else if (atomicAdd(times + s, 1))
+      bad = 1;
+  }
+  __syncthreads();
+  if (bad) {
+    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += kBookThreads / 32) {
+    const int s = slots[i];
+    const int pages = min(pages_of(max(c.lens[s], 0)), c.max_pages);
+    for (int k = lane; k < pages; k += 32) {
+      int32_t* entry = c.table + (size_t)s * c.max_pages + k;
+      const int page = *entry;
+      if (page >= 0 && page < c.n_pages) atomicSub(c.refs + page, 1);
+      *entry = -1;
+    }
+    __syncwarp();
+    if (lane == 0) c.lens[s] = 0;
+  }
+}
+
+// Live pages above the count of live pages move, in order, to the free places below it.
+__global__ void __launch_bounds__(kBookThreads) kv4_compact_kernel(Kv4View c) {
+  pdl_trigger();
+  pdl_wait();
+  int live = 0;
+  for (int p = threadIdx.x; p < c.n_pages; p += kBookThreads) live += c.refs[p] > 0;
+  int n_live;
+  block_scan(live, &n_live);
+  int n_holes = 0, n_moves = 0;
+  for (int base = 0; base < c.n_pages; base += 4 * kBookThreads) {
+    const int p = base + 4 * threadIdx.x;
+    int hole[4], move[4], nh = 0, nm = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = p + e < c.n_pages;
+      const bool used = in && c.refs[p + e] > 0;
+      hole[e] = in && p + e < n_live && !used;
+      move[e] = p + e >= n_live && used;
+      nh += hole[e];
+      nm += move[e];
+    }
+    int th, tm;
+    int rh = n_holes + block_scan(nh, &th), rm = n_moves + block_scan(nm, &tm);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (hole[e]) c.move_dst[rh++] = p + e;
+      if (move[e]) c.move_src[rm++] = p + e;
+    }
+    n_holes += th;
+    n_moves += tm;
+  }
+  __syncthreads();   // as many holes as moves: both lists are whole and visible to the CTA
+  for (int m = threadIdx.x; m < n_moves; m += kBookThreads) {
+    const int s = c.move_src[m], d = c.move_dst[m];
+    c.map[s] = d;
+    c.refs[d] = c.refs[s];
+    c.refs[s] = 0;
+  }
+  if (threadIdx.x == 0) {
+    c.head[KV4_WORD_MOVES] = n_moves;
+    c.head[KV4_WORD_LIVE] = n_live;
+  }
+}
+
+// Page contents: move m takes page move_src[m] to move_dst[m] in every layer.  No page is both a source and a
+// destination, so the order does not matter.  With Remap the page tables follow (c.map of a moved page).
+constexpr int kMoveThreads = 256;
+constexpr int kMoveChunk = kMoveThreads * 16 * 4;   // bytes a CTA copies at a time: 4 loads in flight a thread
+
+template <bool Remap>
+__global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4View c, size_t page_bytes) {
+  pdl_trigger();
+  pdl_wait();
+  const int moves = c.head[KV4_WORD_MOVES];
+  const int per = (int)((page_bytes + kMoveChunk - 1) / kMoveChunk);
+  const long long work = (long long)moves * c.n_layers * per;
+  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+    const int part = (int)(w % per);
+    const int layer = (int)(w / per % c.n_layers), m = (int)(w / per / c.n_layers);
+    const size_t plane = (size_t)layer * c.n_pages;
+    const size_t off = (size_t)part * kMoveChunk;
+    const uint4* s = reinterpret_cast<const uint4*>(c.pool + (plane + c.move_src[m]) * page_bytes + off);
+    uint4* d = reinterpret_cast<uint4*>(c.pool + (plane + c.move_dst[m]) * page_bytes + off);
+    const int n = (int)(min((size_t)kMoveChunk, page_bytes - off) / 16);
+    uint4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e * kMoveThreads + (int)threadIdx.x < n) v[e] = s[e * kMoveThreads + threadIdx.x];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e * kMoveThreads + (int)threadIdx.x < n) d[e * kMoveThreads + threadIdx.x] = v[e];
+  }
+  if (Remap && moves > 0) {
+    const int n_live = c.head[KV4_WORD_LIVE];
+    const long long entries = (long long)c.n_seq * c.max_pages;
+    for (long long i = (long long)blockIdx.x * kMoveThreads + threadIdx.x; i < entries;
+         i += (long long)gridDim.x * kMoveThreads) {
+      const int page = c.table[i];
+      if (page >= n_live && page < c.n_pages) c.table[i] = c.map[page];
+    }
+  }
+}
+
+template <bool Remap>
+cudaError_t launch_moves(const Kv4View& c, int n_sms, cudaStream_t st) {
+  const size_t page_bytes = (size_t)c.n_kv * 72 * c.dh;
+  return launch_k(kv4_move_kernel<Remap>, dim3(8 * n_sms), dim3(kMoveThreads), 0, st, 1, c, page_bytes);
+}
+
+}  // namespace
+
+cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st) {
+  if (c.dh == 128)
+    return r.fp16 ? launch_rows<128, __half>(c, layer, r, write, st)
+                  : launch_rows<128, __nv_bfloat16>(c, layer, r, write, st);
+  return r.fp16 ? launch_rows<64, __half>(c, layer, r, write, st)
+                : launch_rows<64, __nv_bfloat16>(c, layer, r, write, st);
+}
+
+cudaError_t kv4_extend(const Kv4View& c, const int32_t* counts, int n_sms, cudaStream_t st) {
+  const cudaError_t e = launch_k(kv4_extend_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c, counts);
+  return e != cudaSuccess ? e : launch_moves<false>(c, n_sms, st);
+}
+
+cudaError_t kv4_fork(const Kv4View& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
+  return launch_k(kv4_fork_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c, src, dst, n);
+}
+
+cudaError_t kv4_free(const Kv4View& c, const int32_t* slots, int n, cudaStream_t st) {
+  return launch_k(kv4_free_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c, slots, n);
+}
+
+cudaError_t kv4_compact(const Kv4View& c, int n_sms, cudaStream_t st) {
+  const cudaError_t e = launch_k(kv4_compact_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c);
+  return e != cudaSuccess ? e : launch_moves<true>(c, n_sms, st);
+}
+
+}  // namespace dg

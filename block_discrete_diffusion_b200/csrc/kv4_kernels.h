@@ -1,0 +1,61 @@
+// kv4_kernels.h -- internal launch interface between the 4-bit cache's entry points (kv4_api.cu) and its kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "dg_kernels.h"
+
+namespace dg {
+
+// Device view of a cache: the caller's pool and the sections of its book (see dg_kv4_cache in dg.h).
+struct Kv4View {
+  uint8_t* pool;         // [n_layers][n_pages][n_kv][72 d_head] bytes
+  int32_t* head;         // [0] error code, [1] moves of the last page call, [2] live pages of the last compaction,
+                         // [3] error code of a wait (apart, since a wait gives up once it is set)
+  int32_t *lens, *refs, *table;
+  int32_t *move_src, *move_dst, *map;   // scratch of the page calls, n_pages words each
+  int n_layers, n_kv, dh, n_pages, n_seq, max_pages;
+};
+
+enum : int { KV4_WORD_ERR = 0, KV4_WORD_MOVES = 1, KV4_WORD_LIVE = 2, KV4_WORD_WAIT = 3, KV4_HEAD_WORDS = 16 };
+
+// K / V rows of an append or a read: element (seq, row, head, c) at seq * s_seq + row * s_row + head * s_head + c.
+struct Kv4Rows {
+  void *k, *v;
+  long long k_seq, k_row, k_head, v_seq, v_row, v_head;
+  const int32_t* n_rows;   // rows of each sequence (null: `rows` each)
+  int rows;
+  int fp16;                // element type: bf16 (0) or fp16 (1)
+};
+
+cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st);
+
+// page bookkeeping; each is one launch on the book, extend and compact with a second one that moves pages
+cudaError_t kv4_extend(const Kv4View& c, const int32_t* counts, int n_sms, cudaStream_t st);
+cudaError_t kv4_fork(const Kv4View& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st);
+cudaError_t kv4_free(const Kv4View& c, const int32_t* slots, int n, cudaStream_t st);
+cudaError_t kv4_compact(const Kv4View& c, int n_sms, cudaStream_t st);
+
+struct Kv4Attn {
+  const void* q;
+  void* out;
+  float* lse;              // [n_seq][rows][n_q] or null
+  const int32_t* n_rows;
+  long long q_seq, q_row, q_head, o_seq, o_row, o_head;
+  int n_q, rows, causal, fp16;
+  float scale;
+  int n_splits;
+  void* part_o;            // [n_splits][n_seq][rows][n_q][dh] (fp32 or fp16, by the form)
+  float* part_lse;         // [n_splits][n_seq][rows][n_q], base 2
+};
+
+constexpr int kKv4FewRows = 8;    // query rows of one tile of the few-rows form (one n-tile of an m16n8k16)
+cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
+cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool part_fp32, cudaStream_t st);
+
+// kernel attributes are per device: true the first time `done` (one per kernel) meets the current device
+bool first_on_device(unsigned long long* done);
+
+}  // namespace dg

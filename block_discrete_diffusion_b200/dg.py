@@ -17,6 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdg.so")
 
 c_int, c_float, c_void_p, c_size_t, c_uint64 = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint64
+c_int64 = ctypes.c_int64
 
 # the entry points declared in include/dg.h
 ENTRY_POINTS = (
@@ -25,6 +26,8 @@ ENTRY_POINTS = (
     "dg_block_commit", "dg_decode", "dg_layer_forward", "dg_sample_workspace_bytes", "dg_sample", "dg_device_error",
     "dg_temperature", "dg_stats_reset", "dg_stats_read", "dg_sample_noalloc", "dg_sample_noalloc_max_rows",
     "dg_block_commit_last_kv", "dg_head_sample_workspace_bytes", "dg_head_sample", "dg_head_sample_error",
+    "dg_kv4_pool_bytes", "dg_kv4_book_bytes", "dg_kv4_init", "dg_kv4_extend", "dg_kv4_fork", "dg_kv4_free",
+    "dg_kv4_compact", "dg_kv4_append", "dg_kv4_read", "dg_kv4_attend_workspace_bytes", "dg_kv4_attend", "dg_kv4_error",
 )
 
 # dg_kernel_class, in order
@@ -62,6 +65,23 @@ class dg_sampler_params(ctypes.Structure):
                 ("t_end", c_float), ("entropy_bound", c_float), ("stop_mean_entropy", c_float),
                 ("rerand_entropy", c_float), ("seed", c_uint64), ("eos_id", c_int), ("commit_mode", c_int),
                 ("commit_rule", c_int)]
+
+
+class dg_kv4_cache_t(ctypes.Structure):   # the C struct dg_kv4_cache
+    _fields_ = [(n, c_int) for n in ("n_layers", "n_kv", "d_head", "n_pages", "n_seq", "max_pages")] + [
+        ("d_pool", c_void_p), ("pool_bytes", c_size_t), ("d_book", c_void_p), ("book_bytes", c_size_t)]
+
+
+class dg_kv4_rows(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p)] + [
+        (n, c_int64) for n in ("k_seq", "k_row", "k_head", "v_seq", "v_row", "v_head")] + [
+        ("d_rows", c_void_p), ("rows", c_int), ("dtype", c_int)]
+
+
+class dg_kv4_attn(ctypes.Structure):
+    _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("d_rows", c_void_p)] + [
+        (n, c_int64) for n in ("q_seq", "q_row", "q_head", "o_seq", "o_row", "o_head")] + [
+        (n, c_int) for n in ("n_q", "rows", "dtype", "causal")] + [("scale", c_float), ("plan_len", c_int)]
 
 
 def sampler_params(vocab, seed=0, canvas_len=256, max_steps=48, fixed_steps=0, t_start=0.8, t_end=0.4,
@@ -119,6 +139,22 @@ def lib():
         L.dg_head_sample.argtypes = [c_void_p, c_void_p, c_int, c_int, c_int, P(dg_sampler_params), c_int, c_void_p,
                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
         L.dg_head_sample_error.argtypes = [c_void_p, c_void_p, P(c_int)]
+        C = P(dg_kv4_cache_t)
+        L.dg_kv4_pool_bytes.argtypes = [C]
+        L.dg_kv4_pool_bytes.restype = c_size_t
+        L.dg_kv4_book_bytes.argtypes = [C]
+        L.dg_kv4_book_bytes.restype = c_size_t
+        L.dg_kv4_init.argtypes = [C, c_void_p]
+        L.dg_kv4_extend.argtypes = [C, c_void_p, c_void_p]
+        L.dg_kv4_fork.argtypes = [C, c_void_p, c_void_p, c_int, c_void_p]
+        L.dg_kv4_free.argtypes = [C, c_void_p, c_int, c_void_p]
+        L.dg_kv4_compact.argtypes = [C, c_void_p]
+        L.dg_kv4_append.argtypes = [C, c_int, P(dg_kv4_rows), c_void_p]
+        L.dg_kv4_read.argtypes = [C, c_int, P(dg_kv4_rows), c_void_p]
+        L.dg_kv4_attend_workspace_bytes.argtypes = [C, c_int, c_int]
+        L.dg_kv4_attend_workspace_bytes.restype = c_size_t
+        L.dg_kv4_attend.argtypes = [C, c_int, P(dg_kv4_attn), c_void_p, c_size_t, c_void_p]
+        L.dg_kv4_error.argtypes = [C, c_void_p, P(c_int)]
         L.dg_device_error.argtypes = [c_void_p, P(c_int)]
         L.dg_stats_reset.argtypes = [c_void_p, c_int]
         L.dg_stats_read.argtypes = [c_void_p, c_void_p, c_void_p]
@@ -309,6 +345,172 @@ def dg_head_sample_error(ws, stream=None) -> int:
     st = lib().dg_head_sample_error(_ptr(ws), _stream_handle(stream), ctypes.byref(code))
     if st not in (DG_OK, DG_ERR_DEVICE):
         _check("dg_head_sample_error", st)
+    return code.value
+
+
+# ---------------------------------------------------------------------------------------------
+# the paged 4-bit cache
+# ---------------------------------------------------------------------------------------------
+_KV4_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+class Kv4Cache:
+    """A cache's shape and its two buffers (kept alive here).  lens [n_seq], refs [n_pages] and table [n_seq, max_pages]
+    are int32 views of the book: read them as you like, change them through the calls below."""
+
+    def __init__(self, c, pool, book):
+        self.c, self.pool, self.book = c, pool, book
+        self.ref = ctypes.byref(c)
+        self.device = pool.device
+        pad = lambda n: (n + 3) // 4 * 4   # noqa: E731
+        refs = 16 + pad(c.n_seq)
+        table = refs + pad(c.n_pages)
+        self.lens = book[16:16 + c.n_seq]
+        self.refs = book[refs:refs + c.n_pages]
+        self.table = book[table:table + c.n_seq * c.max_pages].view(c.n_seq, c.max_pages)
+
+
+def dg_kv4_cache(n_layers, n_kv, d_head, n_pages, n_seq, max_pages, pool=None, book=None) -> Kv4Cache:
+    """pool (uint8) and book (int32): caller device buffers, taken as they are; allocated here through torch and
+    initialised (every sequence empty) if None."""
+    c = dg_kv4_cache_t(n_layers, n_kv, d_head, n_pages, n_seq, max_pages, None, 0, None, 0)
+    fresh = book is None
+    if (pool is None) != fresh:
+        raise ValueError("give both pool and book, or neither")
+    if fresh:
+        need = dg_kv4_pool_bytes(c)
+        if not need:
+            raise ValueError("dg_kv4_cache: a shape this build does not support")
+        dev = torch.device("cuda", torch.cuda.current_device())
+        pool = torch.empty(need, dtype=torch.uint8, device=dev)
+        book = torch.empty(dg_kv4_book_bytes(c) // 4, dtype=torch.int32, device=dev)
+    if pool.dtype != torch.uint8 or book.dtype != torch.int32 or book.dim() != 1 or pool.device != book.device:
+        raise ValueError("pool must be uint8 and book a flat int32 tensor on one device")
+    c.d_pool, c.pool_bytes, c.d_book, c.book_bytes = _ptr(pool), pool.numel(), _ptr(book), 4 * book.numel()
+    if not dg_kv4_book_bytes(c) or c.book_bytes < dg_kv4_book_bytes(c):
+        raise ValueError("dg_kv4_cache: a shape this build does not support, or a book too small for it")
+    cache = Kv4Cache(c, pool, book)
+    if fresh:
+        dg_kv4_init(cache)
+    return cache
+
+
+def dg_kv4_pool_bytes(c) -> int:
+    return int(lib().dg_kv4_pool_bytes(ctypes.byref(getattr(c, "c", c))))
+
+
+def dg_kv4_book_bytes(c) -> int:
+    return int(lib().dg_kv4_book_bytes(ctypes.byref(getattr(c, "c", c))))
+
+
+def _kv4_stream(cache, stream):
+    """The stream's handle; the kernels run on the current device, so the cache has to lie there."""
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream_handle(stream)
+
+
+def _kv4_ints(cache, t, n, what):
+    """An int32 argument of n values on the cache's device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != cache.device or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what}: expected {n} contiguous int32 values on {cache.device}")
+    return t.data_ptr()
+
+
+def _kv4_tensor(cache, t, shape, what, dtype=None):
+    """A rows argument: its type's code and its strides; channels lie side by side."""
+    code = _KV4_DTYPES.get(t.dtype)
+    if code is None or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected bf16 or fp16, the same for every tensor of the call")
+    if tuple(t.shape) != tuple(shape) or t.device != cache.device:
+        raise ValueError(f"{what}: expected shape {tuple(shape)} on {cache.device}, got {tuple(t.shape)} on {t.device}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{what}: channels must be contiguous")
+    return code, s
+
+
+def dg_kv4_init(cache: Kv4Cache, stream=None):
+    _check("dg_kv4_init", lib().dg_kv4_init(cache.ref, _kv4_stream(cache, stream)))
+
+
+def dg_kv4_extend(cache: Kv4Cache, counts, stream=None):
+    """counts int32 [n_seq]: positions by which each sequence grows."""
+    _check("dg_kv4_extend", lib().dg_kv4_extend(cache.ref, _kv4_ints(cache, counts, cache.c.n_seq, "counts"),
+                                                _kv4_stream(cache, stream)))
+
+
+def dg_kv4_fork(cache: Kv4Cache, src, dst, stream=None):
+    n = src.numel()
+    _check("dg_kv4_fork", lib().dg_kv4_fork(cache.ref, _kv4_ints(cache, src, n, "src"), _kv4_ints(cache, dst, n, "dst"),
+                                            n, _kv4_stream(cache, stream)))
+
+
+def dg_kv4_free(cache: Kv4Cache, slots, stream=None):
+    n = slots.numel()
+    _check("dg_kv4_free", lib().dg_kv4_free(cache.ref, _kv4_ints(cache, slots, n, "slots"), n,
+                                            _kv4_stream(cache, stream)))
+
+
+def dg_kv4_compact(cache: Kv4Cache, stream=None):
+    _check("dg_kv4_compact", lib().dg_kv4_compact(cache.ref, _kv4_stream(cache, stream)))
+
+
+def _kv4_rows(fn, cache, layer, k, v, rows, stream):
+    c = cache.c
+    shape = (c.n_seq, k.shape[1] if k.dim() == 4 else -1, c.n_kv, c.d_head)
+    code, ks = _kv4_tensor(cache, k, shape, "k")
+    _, vs = _kv4_tensor(cache, v, shape, "v", k.dtype)
+    r = dg_kv4_rows(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                    _kv4_ints(cache, rows, c.n_seq, "rows"), shape[1], code)
+    _check(fn, getattr(lib(), fn)(cache.ref, layer, ctypes.byref(r), _kv4_stream(cache, stream)))
+
+
+def dg_kv4_append(cache: Kv4Cache, layer, k, v, rows=None, stream=None):
+    """k, v [n_seq, T, n_kv, d_head] (any strides with contiguous channels) into the last positions of every sequence;
+    rows int32 [n_seq]: how many of the T rows each sequence has (None: all)."""
+    _kv4_rows("dg_kv4_append", cache, layer, k, v, rows, stream)
+
+
+def dg_kv4_read(cache: Kv4Cache, layer, k, v, rows=None, stream=None):
+    """The values of every sequence's last positions into k, v (as dg_kv4_append takes them); rows beyond a sequence's
+    count are left as they were."""
+    _kv4_rows("dg_kv4_read", cache, layer, k, v, rows, stream)
+
+
+def dg_kv4_attend_workspace_bytes(cache: Kv4Cache, n_q, rows) -> int:
+    return int(lib().dg_kv4_attend_workspace_bytes(cache.ref, n_q, rows))
+
+
+def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale=None, causal=False, plan_len=0,
+                  stream=None):
+    """q, out [n_seq, T, n_q, d_head] (any strides with contiguous channels), lse fp32 [n_seq, T, n_q]; scale defaults to
+    d_head^-0.5; rows as in dg_kv4_append."""
+    c = cache.c
+    if q.dim() != 4:
+        raise ValueError("q: expected [n_seq, T, n_q, d_head]")
+    shape = (c.n_seq, q.shape[1], q.shape[2], c.d_head)
+    code, qs = _kv4_tensor(cache, q, shape, "q")
+    _, os_ = _kv4_tensor(cache, out, shape, "out", q.dtype)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != shape[:3] or not lse.is_contiguous()
+                            or lse.device != cache.device):
+        raise ValueError(f"lse: expected a contiguous fp32 tensor {shape[:3]} on {cache.device}")
+    if ws.device != cache.device:
+        raise ValueError(f"ws: expected a buffer on {cache.device}")
+    a = dg_kv4_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                    _kv4_ints(cache, rows, c.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],
+                    shape[1], code, int(bool(causal)), c.d_head ** -0.5 if scale is None else scale, plan_len)
+    _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), _ptr(ws),
+                                                ws.numel() * ws.element_size(), _kv4_stream(cache, stream)))
+
+
+def dg_kv4_error(cache: Kv4Cache, stream=None) -> int:
+    code = c_int()
+    st = lib().dg_kv4_error(cache.ref, _kv4_stream(cache, stream), ctypes.byref(code))
+    if st not in (DG_OK, DG_ERR_DEVICE):
+        _check("dg_kv4_error", st)
     return code.value
 
 

@@ -259,6 +259,115 @@ dg_status dg_head_sample(const void *d_xn, const void *d_head, int d_model, int 
                          size_t ws_bytes, void *stream);
 dg_status dg_head_sample_error(void *ws, void *stream, int *h_code);
 
+/* ------------------------------------------------------------------------------------------------
+ * A paged key / value cache held in 4 bits, and attention over it.
+ *
+ * For callers that keep many long prefixes: 4.5 bits a value instead of 16, pages of 64 positions that
+ * sequences may share (one prompt, several continuations), and memory that comes back page by page.
+ * Like dg_sample these calls take caller buffers and no handle; nothing is allocated.
+ *
+ * A value is code * scale: a code of 4 bits (e2m1: a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale
+ * byte for 16 neighbouring channels of one position (ue5m3: exponent bias 15, 3 mantissa bits, subnormal
+ * below 2^-14; the byte shifted left by 7 is that number as an fp16).  scale = round(largest magnitude of
+ * the 16 / 6), code = round(value / scale), both to nearest, ties to even.  Scales end at 10240, so
+ * magnitudes beyond 61440, infinities among them, become 61440; 16 values with a NaN among them all become NaN.
+ * Code * scale is exact in bf16 and fp16.
+ *
+ * The book is int32 words that belong to the library: 16 words of status, the lengths [n_seq], the
+ * reference counts [n_pages], the page tables [n_seq][max_pages] (-1: no page) and scratch; each section is
+ * padded to 4 words.  A copy of the book (and of the pages it names) is a snapshot.  The pool is
+ * [n_layers][n_pages][n_kv][72 d_head] bytes; the 72 d_head bytes of 64 positions of a head hold K's codes,
+ * V's codes, K's scales and V's scales in the order of the tensor-core fragments that read them.
+ *
+ * Calls on one cache share its book, so they must be ordered (one stream, or events).  Checks that need device
+ * data happen in the kernels: a call that fails them changes nothing (rows of the sequence at fault are
+ * skipped) and records a code for dg_kv4_error: 5 an index out of range, a page written that has other
+ * owners, or a sequence named twice; 7 too few free pages; 8 a count that does not fit its sequence.
+ * ------------------------------------------------------------------------------------------------ */
+#define DG_KV4_PAGE 64   /* positions of a page */
+
+/* d_head 64 or 128; n_seq <= 4096, n_pages and max_pages (of one sequence) <= 2^24, n_seq * max_pages < 2^30,
+ * n_seq * n_kv <= 65535.  Buffers 16-byte aligned, of at least dg_kv4_pool_bytes / dg_kv4_book_bytes. */
+typedef struct {
+  int n_layers, n_kv, d_head, n_pages, n_seq, max_pages;
+  void *d_pool;
+  size_t pool_bytes;
+  void *d_book;
+  size_t book_bytes;
+} dg_kv4_cache;
+
+/* Element types of rows. */
+#define DG_DTYPE_BF16 0
+#define DG_DTYPE_FP16 1
+
+/* Sizes for a cache's shape (the buffers are not looked at); 0 for a shape this build does not support. */
+size_t dg_kv4_pool_bytes(const dg_kv4_cache *c);
+size_t dg_kv4_book_bytes(const dg_kv4_cache *c);
+
+/* Every sequence empty, every page free.  The pool need not be cleared. */
+dg_status dg_kv4_init(const dg_kv4_cache *c, void *stream);
+
+/* Each sequence s grows by d_counts[s] >= 0 positions (int32 [n_seq]): its length, and the pages it needs
+ * (lowest free pages first, sequences in ascending order).  A sequence that grows into a partly filled page with
+ * other owners gets a copy of its own first.  The new positions' contents are whatever the pages held. */
+dg_status dg_kv4_extend(const dg_kv4_cache *c, const int32_t *d_counts, void *stream);
+
+/* Sequence d_dst[i] (empty, named once, no source itself) becomes a second owner of sequence d_src[i]'s pages, i < n. */
+dg_status dg_kv4_fork(const dg_kv4_cache *c, const int32_t *d_src, const int32_t *d_dst, int n, void *stream);
+
+/* The sequences d_slots[i], i < n, each named once, become empty; pages without owners are free. */
+dg_status dg_kv4_free(const dg_kv4_cache *c, const int32_t *d_slots, int n, void *stream);
+
+/* The pages in use move to the lowest places of the pool: n of them fill pages 0 .. n-1 (those above move, in
+ * ascending order, to the free places below, in ascending order), and the tables follow. */
+dg_status dg_kv4_compact(const dg_kv4_cache *c, void *stream);
+
+/* Rows of K and V in or out.  Element (sequence, row, head, channel) of k lies at k_seq * sequence + k_row * row +
+ * k_head * head + channel elements behind k; v likewise.  Rows are 16-byte aligned (strides are multiples of 8).
+ * Row j of sequence s is position len - n + j, n = d_rows[s] (null: rows) and 0 <= n <= min(rows, len). */
+typedef struct {
+  void *k, *v;
+  int64_t k_seq, k_row, k_head, v_seq, v_row, v_head;
+  const int32_t *d_rows;
+  int rows, dtype;
+} dg_kv4_rows;
+
+/* Quantise the rows into the sequences' last positions of one layer (dg_kv4_extend made room for them).  A
+ * page with other owners is not written. */
+dg_status dg_kv4_append(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);
+/* The values that the sequences' last positions of one layer stand for (exact in both types). */
+dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);
+
+/* Attention of n = d_rows[s] (null: rows) query rows of every sequence over its cached positions:
+ * out = softmax(scale * q k^T) v.  causal = 0: every row sees all of [0, len) (a canvas whose own K / V are in the
+ * cache); causal = 1: row j is position len - n + j and sees itself and what comes before (a prompt chunk,
+ * a single token).  A row that sees nothing is 0 with lse -inf.  Query head h reads KV head h / (n_q / n_kv).
+ * Element (s, j, h, c) of q lies at q_seq * s + q_row * j + q_head * h + c elements (strides multiples of 8, rows
+ * 16-byte aligned), out likewise; both of type dtype.  lse (nullable): fp32 [n_seq][rows][n_q], the natural
+ * logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  plan_len: the longest length
+ * to plan the key splits for (0: max_pages * 64); any length is computed right.  NaN and infinities: stale
+ * contents behind a sequence's end never matter; a NaN among its cached values reaches every row of the call that
+ * reads that page, also rows that the causal mask keeps from that position. */
+typedef struct {
+  const void *q;
+  void *out;
+  float *lse;
+  const int32_t *d_rows;
+  int64_t q_seq, q_row, q_head, o_seq, o_row, o_head;
+  int n_q, rows, dtype, causal;
+  float scale;
+  int plan_len;
+} dg_kv4_attn;
+
+/* ws: device scratch, used by one call at a time. */
+size_t dg_kv4_attend_workspace_bytes(const dg_kv4_cache *c, int n_q, int rows);
+dg_status dg_kv4_attend(const dg_kv4_cache *c, int layer, const dg_kv4_attn *a, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/* Synchronise the stream and return the first device-side error code recorded in the book since the last call
+ * (0 = none); the record is cleared.  Returns DG_ERR_DEVICE if non-zero. */
+dg_status dg_kv4_error(const dg_kv4_cache *c, void *stream, int *h_code);
+
 /* Synchronise the handle's stream and return the first device-side error code recorded since the
  * last call (0 = none) in *h_code; the record is cleared.  Returns DG_ERR_DEVICE if non-zero. */
 dg_status dg_device_error(dg_seqs *s, int *h_code);

@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["dg_api.cu", "gemm.cu", "attention.cu", "misc.cu", "sampler.cu", "sampler_noalloc.cu", "dequant.cu",
-           "head_sampler.cu", "expert_fp8.cu", "kv4_api.cu", "kv4_cache.cu", "kv4_attention.cu"]
+           "head_sampler.cu", "expert_fp8.cu", "kv4_api.cu", "kv4_cache.cu", "kv4_attention.cu", "kv4_canvas.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -89,14 +89,34 @@ int current_sms() {
   return n;
 }
 
-// Key splits of the few-rows form: enough CTAs to fill the SMs once, at least one page for each of a CTA's warps.
-constexpr int kMaxSplits = 64;
-int few_splits(const dg_kv4_cache* c, int n_q, int rows, long long plan_len) {
-  const long long tiles = ((long long)rows * (n_q / c->n_kv) + kKv4FewRows - 1) / kKv4FewRows;
-  const long long units = tiles * c->n_seq * c->n_kv;
-  const long long slots = (long long)current_sms() * (c->d_head == 128 ? 2 : 4);
-  const long long pages = (plan_len + DG_KV4_PAGE - 1) / DG_KV4_PAGE;
-  return (int)std::max(1ll, std::min({(long long)kMaxSplits, slots / units, (pages + 3) / 4}));
+// How a call's work is divided: the form, and the CTAs among which it goes.
+struct Plan {
+  bool few;
+  int n_ctas, min_share;
+  size_t tile, row_bytes;   // rows of a workspace slot, bytes of a row in it
+  size_t bytes(const dg_kv4_cache* c) const { return line_bytes(c) + 2 * (size_t)n_ctas * tile * (row_bytes + 4); }
+  static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
+};
+
+// Rows of a KV head up to which the few-rows form runs.
+constexpr int kFewRows = 16;
+
+Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
+  Plan p;
+  p.few = (long long)rows * (n_q / c->n_kv) <= kFewRows;
+  const int sms = current_sms();
+  if (p.few) {
+    p.n_ctas = sms * (c->d_head == 128 ? 2 : 4);   // what fits the SMs' shared memory at once
+    p.min_share = 4;                               // a page for each warp
+    p.tile = kKv4FewTile;
+    p.row_bytes = 4 * (size_t)c->d_head;
+  } else {
+    p.n_ctas = sms;                                // one CTA holds an SM
+    p.min_share = 1;
+    p.tile = kKv4ManyTile;
+    p.row_bytes = 2 * (size_t)c->d_head;
+  }
+  return p;
 }
 
 dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_kv4_rows* r) {
@@ -180,9 +200,8 @@ DG_API dg_status dg_kv4_read(const dg_kv4_cache* c, int layer, const dg_kv4_rows
 }
 
 DG_API size_t dg_kv4_attend_workspace_bytes(const dg_kv4_cache* c, int n_q, int rows) {
-  if (shape_error(c) || n_q <= 0 || n_q % c->n_kv || rows <= 0) return 0;
-  const size_t splits = few_splits(c, n_q, rows, (long long)c->max_pages * DG_KV4_PAGE);
-  return splits * c->n_seq * rows * n_q * (4 * (size_t)c->d_head + 4) + 1024;
+  if (shape_error(c) || n_q <= 0 || n_q % c->n_kv || n_q > 8192 || rows <= 0 || rows > 65536) return 0;
+  return plan_of(c, n_q, rows).bytes(c) + 256;
 }
 
 DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_attn* a, void* ws, size_t ws_bytes,
@@ -193,17 +212,15 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   if (!a || !aligned16(a->q) || !aligned16(a->out)) return bad(fn, "q and out must be 16-byte aligned device buffers");
   if (layer < 0 || layer >= c->n_layers) return bad(fn, "layer out of range");
   if (a->dtype != DG_DTYPE_BF16 && a->dtype != DG_DTYPE_FP16) return bad(fn, "dtype must be bf16 or fp16");
-  if (a->n_q <= 0 || a->n_q % c->n_kv) return bad(fn, "n_q must be a positive multiple of n_kv");
+  if (a->n_q <= 0 || a->n_q % c->n_kv || a->n_q > 8192) return bad(fn, "n_q must be a multiple of n_kv in [1, 8192]");
   if (a->rows <= 0 || a->rows > 65536) return bad(fn, "rows must be in [1, 65536]");
   if (a->causal != 0 && a->causal != 1) return bad(fn, "causal must be 0 or 1");
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return bad(fn, "scale must be positive and finite");
-  if (a->plan_len < 0) return bad(fn, "plan_len must not be negative");
   if ((a->q_seq | a->q_row | a->q_head | a->o_seq | a->o_row | a->o_head) & 7)
     return bad(fn, "strides must be multiples of 8 elements");
   if (!ws || ws_bytes < dg_kv4_attend_workspace_bytes(c, a->n_q, a->rows))
     return bad(fn, "workspace too small", DG_ERR_CAPACITY);
-  const long long most = (long long)c->max_pages * DG_KV4_PAGE;
-  const long long plan = a->plan_len > 0 ? std::min<long long>(a->plan_len, most) : most;
+  const Plan p = plan_of(c, a->n_q, a->rows);
   Kv4Attn k{};
   k.q = a->q;
   k.out = a->out;
@@ -220,15 +237,16 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   k.causal = a->causal;
   k.fp16 = a->dtype == DG_DTYPE_FP16;
   k.scale = a->scale;
-  k.n_splits = few_splits(c, a->n_q, a->rows, plan);
+  k.n_ctas = p.n_ctas;
+  k.min_share = p.min_share;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
-  const size_t n = (size_t)k.n_splits * c->n_seq * a->rows * a->n_q;
-  k.part_o = base;
-  k.part_lse = reinterpret_cast<float*>(base + n * c->d_head * 4);
+  k.line = base;
+  k.part_o = base + Plan::line_bytes(c);
+  k.part_lse = reinterpret_cast<float*>(base + Plan::line_bytes(c) + 2 * (size_t)p.n_ctas * p.tile * p.row_bytes);
   const Kv4View v = view(c);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = kv4_attend_few(v, layer, k, s);
-  if (e == cudaSuccess && k.n_splits > 1) e = kv4_attend_merge(v, k, true, s);
+  cudaError_t e = p.few ? kv4_attend_few(v, layer, k, s) : kv4_attend_many(v, layer, k, s);
+  if (e == cudaSuccess) e = kv4_attend_merge(v, k, p.few, s);
   return launched(fn, e);
 }
 

@@ -6,8 +6,7 @@
 // and p in [0, 1] is rounded once, by 2^-11 of itself at most.
 #include <math.h>
 
-#include "kv4.cuh"
-#include "kv4_kernels.h"
+#include "kv4_attention.cuh"
 
 namespace dg {
 
@@ -32,30 +31,10 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   return d;
 }
 
-// What a sequence's rows see: its length and row count, checked against what the tables can hold.
-struct SeqView {
-  int len, n;
-};
-__device__ __forceinline__ SeqView seq_view(const Kv4View& c, const Kv4Attn& a, int seq) {
-  SeqView v;
-  v.len = c.lens[seq];
-  v.n = a.n_rows ? a.n_rows[seq] : a.rows;
-  if (v.len < 0 || (long long)v.len > (long long)c.max_pages * kPage || v.n < 0 || v.n > a.rows) {
-    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_COUNT);
-    v.len = v.n = 0;
-  }
-  return v;
-}
-// positions that row j of n sees
-__device__ __forceinline__ int row_limit(const SeqView& v, int j, int causal) {
-  return causal ? max(0, min(v.len, v.len - v.n + j + 1)) : v.len;
-}
-
 // ---------------------------------------------------------------------------------------------
 // few rows: single tokens and other tiles of at most 8 rows of a KV head
 // ---------------------------------------------------------------------------------------------
-// Grid (row tile, split, sequence x KV head), 4 warps; a warp takes every fourth page of the split.  It keeps a ring
-// of whole blocks in shared memory (one bulk copy each: a block is contiguous), dequantises them into
+// 4 warps; a warp takes every fourth page of the CTA's piece of a unit.  It keeps a ring of whole blocks in shared memory (one bulk copy each: a block is contiguous), dequantises them into
 // m16n8k16 fragments and multiplies S = K Q^T and O^T += V^T P^T: positions and channels are the 16-wide
 // side, the rows the 8-wide one, so a tile of 8 rows wastes no tensor work, and a row's statistics lie with the same
 // lanes in S and in O^T.  Bound by the cache's bytes: mma.sync is enough, since 8 rows x 2 operations a value
@@ -67,7 +46,7 @@ template <int DH>
 struct FewSmem {
   alignas(16) uint8_t ring[kFewWarps][kFewStages][Kv4<DH>::kBytes];
   uint64_t full[kFewWarps][kFewStages];
-  float m[kFewWarps][kKv4FewRows], l[kFewWarps][kKv4FewRows];
+  float m[kFewWarps][kKv4FewTile], l[kFewWarps][kKv4FewTile];
 };
 
 template <int DH, typename T>
@@ -86,291 +65,304 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   __syncwarp();
   pdl_wait();
 
-  const int seq = blockIdx.z / c.n_kv, head = blockIdx.z % c.n_kv, split = blockIdx.y;
   const int G = a.n_q / c.n_kv;
-  const SeqView sv = seq_view(c, a, seq);
-  const int r0 = blockIdx.x * kKv4FewRows;      // row r of the group: query row r / G, head r % G of the group
-  const int nr = min(kKv4FewRows, sv.n * G - r0);
-  if (nr <= 0) return;
-  const int limit = row_limit(sv, (r0 + nr - 1) / G, a.causal);   // the tile's last row sees the most
-  const int all = row_limit(sv, r0 / G, a.causal);                // every row sees positions below this
-  const int pages = (limit + kPage - 1) / kPage;
-  const int per = (pages + a.n_splits - 1) / a.n_splits;
-  const int p0 = split * per, p1 = min(pages, p0 + per);
-  const int n_mine = p1 - p0 > warp ? (p1 - p0 - warp + kFewWarps - 1) / kFewWarps : 0;
+  Stretch stretch = find_stretch<kKv4FewTile, kKv4FewStep, 32 * kFewWarps>(c, a);
+  Piece pc;
+  int phase = 0;                // copies that each stage of the ring has seen, one bit each: its barrier's parity
+  while (next_piece<kKv4FewTile, kKv4FewStep>(c, a, stretch, pc)) {
+    const int seq = pc.seq, head = pc.head;
+    const SeqView sv = pc.v;
+    const int r0 = pc.tile * kKv4FewTile;         // row r of the group: query row r / G, head r % G of the group
+    const int nr = min(kKv4FewTile, sv.n * G - r0);
+    const int limit = row_limit(sv, (r0 + nr - 1) / G, a.causal);   // the tile's last row sees the most
+    const int all = row_limit(sv, r0 / G, a.causal);                // every row sees positions below this
+    const int p0 = pc.s0, p1 = min((limit + kPage - 1) / kPage, pc.s1);
+    const int n_mine = p1 - p0 > warp ? (p1 - p0 - warp + kFewWarps - 1) / kFewWarps : 0;
 
-  // page i of this warp: p0 + warp + 4 i; ids are read 32 at a time, one a lane
-  const int32_t* table = c.table + (size_t)seq * c.max_pages + p0 + warp;
-  int ids = 0;
-  auto page_id = [&](int i) {   // whole warp, i ascending
-    if ((i & 31) == 0) {
-      ids = -1;
-      if (i + lane < n_mine) {
-        ids = table[(i + lane) * kFewWarps];
-        if (ids < 0 || ids >= c.n_pages) {
-          report_error(c.head, DEV_ERR_BAD_INDEX);
-          ids = -1;
-        }
-      }
-    }
-    return __shfl_sync(0xffffffffu, ids, i & 31);
-  };
-  const uint8_t* plane = c.pool + ((size_t)layer * c.n_pages * c.n_kv + head) * F::kBytes;
-  auto fetch = [&](int i) {     // whole warp: start the copy of its page i; a page that is not there is not copied
-    const int id = page_id(i);
-    if (lane == 0) {
-      uint64_t* bar = &sm.full[warp][i % kFewStages];
-      if (id >= 0) {
-        mbar_arrive_expect_tx(bar, F::kBytes);
-        bulk_load(bar, sm.ring[warp][i % kFewStages], plane + (size_t)id * c.n_kv * F::kBytes, F::kBytes);
-      } else {
-        mbar_arrive(bar);
-      }
-    }
-    return id >= 0;
-  };
-  uint32_t present = 0;         // by stage
-  for (int i = 0; i < kFewStages && i < n_mine; ++i) present |= (uint32_t)fetch(i) << i;
-
-  // Q fragments: row g, channels DH/4 t + 4 j + {0..3}, times a power of two that makes them exact in fp16
-  uint32_t qf[NJ][2];
-  float fac[2];                 // rows 2t, 2t + 1: scale log2(e) and the power of two taken out
-  {
-    const int r = r0 + g;
-    float x[DH / 4];
-#pragma unroll
-    for (int i = 0; i < DH / 4; ++i) x[i] = 0.f;
-    if (g < nr) {
-      const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + (r / G) * a.q_row + (head * G + r % G) * a.q_head +
-                   DH / 4 * t;
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(q)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[8 * i + 2 * e] = Half<T>::lo(w[e]);
-          x[8 * i + 2 * e + 1] = Half<T>::hi(w[e]);
-        }
-      }
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < DH / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // the row's largest value between 2^14 and 2^15: what fp16 then loses is below 2^-39 of it (the exponent is
-    // kept where both powers are normal numbers)
-    const int e = min(253, max(15, (int)((__float_as_uint(amax) >> 23) & 255))) - 127;
-    const float down = __uint_as_float((uint32_t)(141 - e) << 23), up = __uint_as_float((uint32_t)(113 + e) << 23);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      qf[j][0] = pack_f16x2(x[4 * j] * down, x[4 * j + 1] * down);
-      qf[j][1] = pack_f16x2(x[4 * j + 2] * down, x[4 * j + 3] * down);
-    }
-    const float f = a.scale * 1.4426950408889634f * up;
-    fac[0] = __shfl_sync(0xffffffffu, f, 8 * t);
-    fac[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-  }
-  int lim[2];                   // positions that rows 2t, 2t + 1 see
-#pragma unroll
-  for (int e = 0; e < 2; ++e) lim[e] = 2 * t + e < nr ? row_limit(sv, (r0 + 2 * t + e) / G, a.causal) : 0;
-
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[NJ][4];               // O^T: channels DH/8 g + 2 j + {0, 1}, rows 2t, 2t + 1
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-  bool ok = true;
-  for (int i = 0; i < n_mine; ++i) {
-    const int st = i % kFewStages;
-    ok = ok && mbar_wait(&sm.full[warp][st], (i / kFewStages) & 1, c.head + KV4_WORD_WAIT, DEV_ERR_TIMEOUT_ATTN);
-    if (!__all_sync(0xffffffffu, ok)) break;
-    const bool here = (present >> st) & 1;
-    const int base = (p0 + warp + i * kFewWarps) * kPage;
-    if (here) {
-      const uint8_t* block = sm.ring[warp][st];
-      float s[4][4];
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
-        // scales of positions g and g + 8 of the tile, kH blocks each
-        const uint8_t* sc = block + F::kSk + lane * 8 * F::kH + 2 * kt * F::kH;
-        const uint32_t sw = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
-#pragma unroll
-        for (int jh = 0; jh < F::kH; ++jh) {
-          const uint4 q = *reinterpret_cast<const uint4*>(block + ((kt * F::kH + jh) * 32 + lane) * 16);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          uint32_t s0, s1;
-          if constexpr (F::kH == 2) {
-            s0 = jh ? scale_pair<1, 1>(sw) : scale_pair<0, 0>(sw);
-            s1 = jh ? scale_pair<3, 3>(sw) : scale_pair<2, 2>(sw);
-          } else {
-            s0 = scale_pair<0, 0>(sw);
-            s1 = scale_pair<1, 1>(sw);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t f[4];
-            e2m1_to_f16(w[j], f);
-            const uint32_t af[4] = {mul_f16x2(f[0], s0), mul_f16x2(f[1], s1), mul_f16x2(f[2], s0), mul_f16x2(f[3], s1)};
-            mma_16816(s[kt], af, qf[4 * jh + j][0], qf[4 * jh + j][1]);
+    // page i of this warp: p0 + warp + 4 i; ids are read 32 at a time, one a lane
+    const int32_t* table = c.table + (size_t)seq * c.max_pages + p0 + warp;
+    int ids = 0;
+    auto page_id = [&](int i) {   // whole warp, i ascending
+      if ((i & 31) == 0) {
+        ids = -1;
+        if (i + lane < n_mine) {
+          ids = table[(i + lane) * kFewWarps];
+          if (ids < 0 || ids >= c.n_pages) {
+            report_error(c.head, DEV_ERR_BAD_INDEX);
+            ids = -1;
           }
         }
       }
-      // base-2 scores, masked; the block's row maxima over the positions (lanes with the same t)
-      float top[2] = {-INFINITY, -INFINITY};
-      const bool whole = base + kPage <= all && nr == kKv4FewRows;
-#pragma unroll
-      for (int kt = 0; kt < 4; ++kt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = s[kt][e] * fac[e & 1];
-          if (!whole && base + kt * 16 + g + 8 * (e >> 1) >= lim[e & 1]) v = -INFINITY;
-          s[kt][e] = v;
-          top[e & 1] = max_nan(top[e & 1], v);
+      return __shfl_sync(0xffffffffu, ids, i & 31);
+    };
+    const uint8_t* plane = c.pool + ((size_t)layer * c.n_pages * c.n_kv + head) * F::kBytes;
+    auto fetch = [&](int i) {     // whole warp: start the copy of its page i; a page that is not there is not copied
+      const int id = page_id(i);
+      if (lane == 0) {
+        uint64_t* bar = &sm.full[warp][i % kFewStages];
+        if (id >= 0) {
+          mbar_arrive_expect_tx(bar, F::kBytes);
+          bulk_load(bar, sm.ring[warp][i % kFewStages], plane + (size_t)id * c.n_kv * F::kBytes, F::kBytes);
+        } else {
+          mbar_arrive(bar);
         }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 4));
-        top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 8));
-        top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 16));
       }
-      const float n0 = max_nan(m[0], top[0]), n1 = max_nan(m[1], top[1]);   // (a NaN score makes its row NaN)
-      if (__any_sync(0xffffffffu, n0 != m[0] || n1 != m[1])) {
-        const float f0 = n0 == m[0] ? 1.f : fast_exp2(m[0] - n0), f1 = n1 == m[1] ? 1.f : fast_exp2(m[1] - n1);
-        l[0] *= f0;
-        l[1] *= f1;
+      return id >= 0;
+    };
+    uint32_t present = 0;         // by stage
+    for (int i = 0; i < kFewStages && i < n_mine; ++i) present |= (uint32_t)fetch(i) << i;
+
+    // Q fragments: row g, channels DH/4 t + 4 j + {0..3}, times a power of two that makes them exact in fp16
+    uint32_t qf[NJ][2];
+    float fac[2];                 // rows 2t, 2t + 1: scale log2(e) and the power of two taken out
+    {
+      const int r = r0 + g;
+      float x[DH / 4];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          o[j][0] *= f0;
-          o[j][1] *= f1;
-          o[j][2] *= f0;
-          o[j][3] *= f1;
-        }
-        m[0] = n0;
-        m[1] = n1;
-      }
-      // a row that sees nothing yet keeps m = -inf: its scores are -inf, its p 0
-      const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-      uint32_t pf[4][2];
+      for (int i = 0; i < DH / 4; ++i) x[i] = 0.f;
+      if (g < nr) {
+        const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + (r / G) * a.q_row + (head * G + r % G) * a.q_head +
+                     DH / 4 * t;
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        const float q0 = fast_exp2(s[kt][0] - b0), q1 = fast_exp2(s[kt][1] - b1);
-        const float q2 = fast_exp2(s[kt][2] - b0), q3 = fast_exp2(s[kt][3] - b1);
-        l[0] += q0 + q2;
-        l[1] += q1 + q3;
-        pf[kt][0] = transpose_8x8(pack_f16x2(q0, q1));   // [position g][row 2t, 2t+1] -> [row g][positions 2t, 2t+1]
-        pf[kt][1] = transpose_8x8(pack_f16x2(q2, q3));
-      }
-      const int left = sv.len - base;   // V of positions at or beyond the length is stale: its scale becomes 0
+        for (int i = 0; i < DH / 32; ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(q)[i];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt) {
-        const int blk = F::kH == 2 ? g : g >> 1;
-        uint32_t sw = *reinterpret_cast<const uint32_t*>(block + F::kSv + (blk * 4 + t) * 16 + 4 * kt);
-        if (left < kPage) {
-          const int pos = kt * 16 + 2 * t;
-          uint32_t keep = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) keep |= pos + (e & 1) + 8 * (e >> 1) < left ? 0xffu << (8 * e) : 0u;
-          sw &= keep;
-        }
-        const uint32_t s01 = scale_pair<0, 1>(sw), s23 = scale_pair<2, 3>(sw);
-#pragma unroll
-        for (int jh = 0; jh < F::kH; ++jh) {
-          const uint4 q = *reinterpret_cast<const uint4*>(block + F::kV + ((kt * F::kH + jh) * 32 + lane) * 16);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t f[4];
-            e2m1_to_f16(w[j], f);
-            const uint32_t af[4] = {mul_f16x2(f[0], s01), mul_f16x2(f[1], s01), mul_f16x2(f[2], s23),
-                                    mul_f16x2(f[3], s23)};
-            mma_16816(o[4 * jh + j], af, pf[kt][0], pf[kt][1]);
+          for (int e = 0; e < 4; ++e) {
+            x[8 * i + 2 * e] = Half<T>::lo(w[e]);
+            x[8 * i + 2 * e + 1] = Half<T>::hi(w[e]);
           }
         }
       }
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < DH / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      float down, up;
+      row_powers(amax, down, up);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        qf[j][0] = pack_f16x2(x[4 * j] * down, x[4 * j + 1] * down);
+        qf[j][1] = pack_f16x2(x[4 * j + 2] * down, x[4 * j + 3] * down);
+      }
+      const float f = a.scale * 1.4426950408889634f * up;
+      fac[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      fac[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
-    __syncwarp();   // every lane has read the stage
-    if (i + kFewStages < n_mine) {
-      const bool again = fetch(i + kFewStages);
-      present = (present & ~(1u << st)) | ((uint32_t)again << st);
+    int lim[2];                   // positions that rows 2t, 2t + 1 see
+#pragma unroll
+    for (int e = 0; e < 2; ++e) lim[e] = 2 * t + e < nr ? row_limit(sv, (r0 + 2 * t + e) / G, a.causal) : 0;
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NJ][4];               // O^T: channels DH/8 g + 2 j + {0, 1}, rows 2t, 2t + 1
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n_mine; ++i) {
+      const int st = i % kFewStages;
+      ok = ok && mbar_wait(&sm.full[warp][st], (phase >> st) & 1, c.head + KV4_WORD_WAIT, DEV_ERR_TIMEOUT_ATTN);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      phase ^= 1 << st;
+      const bool here = (present >> st) & 1;
+      const int base = (p0 + warp + i * kFewWarps) * kPage;
+      if (here) {
+        const uint8_t* block = sm.ring[warp][st];
+        float s[4][4];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
+          // scales of positions g and g + 8 of the tile, kH blocks each
+          const uint8_t* sc = block + F::kSk + lane * 8 * F::kH + 2 * kt * F::kH;
+          const uint32_t sw = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
+#pragma unroll
+          for (int jh = 0; jh < F::kH; ++jh) {
+            const uint4 q = *reinterpret_cast<const uint4*>(block + ((kt * F::kH + jh) * 32 + lane) * 16);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint32_t s0, s1;
+            if constexpr (F::kH == 2) {
+              s0 = jh ? scale_pair<1, 1>(sw) : scale_pair<0, 0>(sw);
+              s1 = jh ? scale_pair<3, 3>(sw) : scale_pair<2, 2>(sw);
+            } else {
+              s0 = scale_pair<0, 0>(sw);
+              s1 = scale_pair<1, 1>(sw);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t f[4];
+              e2m1_to_f16(w[j], f);
+              const uint32_t af[4] = {mul_f16x2(f[0], s0), mul_f16x2(f[1], s1), mul_f16x2(f[2], s0), mul_f16x2(f[3], s1)};
+              mma_16816(s[kt], af, qf[4 * jh + j][0], qf[4 * jh + j][1]);
+            }
+          }
+        }
+        // base-2 scores, masked; the block's row maxima over the positions (lanes with the same t)
+        float top[2] = {-INFINITY, -INFINITY};
+        const bool whole = base + kPage <= all && nr == kKv4FewTile;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = s[kt][e] * fac[e & 1];
+            if (!whole && base + kt * 16 + g + 8 * (e >> 1) >= lim[e & 1]) v = -INFINITY;
+            s[kt][e] = v;
+            top[e & 1] = max_nan(top[e & 1], v);
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 4));
+          top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 8));
+          top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 16));
+        }
+        const float n0 = max_nan(m[0], top[0]), n1 = max_nan(m[1], top[1]);   // (a NaN score makes its row NaN)
+        if (__any_sync(0xffffffffu, n0 != m[0] || n1 != m[1])) {
+          const float f0 = n0 == m[0] ? 1.f : fast_exp2(m[0] - n0), f1 = n1 == m[1] ? 1.f : fast_exp2(m[1] - n1);
+          l[0] *= f0;
+          l[1] *= f1;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            o[j][0] *= f0;
+            o[j][1] *= f1;
+            o[j][2] *= f0;
+            o[j][3] *= f1;
+          }
+          m[0] = n0;
+          m[1] = n1;
+        }
+        // a row that sees nothing yet keeps m = -inf: its scores are -inf, its p 0
+        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+        uint32_t pf[4][2];
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const float q0 = fast_exp2(s[kt][0] - b0), q1 = fast_exp2(s[kt][1] - b1);
+          const float q2 = fast_exp2(s[kt][2] - b0), q3 = fast_exp2(s[kt][3] - b1);
+          l[0] += q0 + q2;
+          l[1] += q1 + q3;
+          pf[kt][0] = transpose_8x8(pack_f16x2(q0, q1));   // [position g][row 2t, 2t+1] -> [row g][positions 2t, 2t+1]
+          pf[kt][1] = transpose_8x8(pack_f16x2(q2, q3));
+        }
+        const int left = sv.len - base;   // V of positions at or beyond the length is stale: its scale becomes 0
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {
+          const int blk = F::kH == 2 ? g : g >> 1;
+          uint32_t sw = *reinterpret_cast<const uint32_t*>(block + F::kSv + (blk * 4 + t) * 16 + 4 * kt);
+          if (left < kPage) {
+            const int pos = kt * 16 + 2 * t;
+            uint32_t keep = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) keep |= pos + (e & 1) + 8 * (e >> 1) < left ? 0xffu << (8 * e) : 0u;
+            sw &= keep;
+          }
+          const uint32_t s01 = scale_pair<0, 1>(sw), s23 = scale_pair<2, 3>(sw);
+#pragma unroll
+          for (int jh = 0; jh < F::kH; ++jh) {
+            const uint4 q = *reinterpret_cast<const uint4*>(block + F::kV + ((kt * F::kH + jh) * 32 + lane) * 16);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t f[4];
+              e2m1_to_f16(w[j], f);
+              const uint32_t af[4] = {mul_f16x2(f[0], s01), mul_f16x2(f[1], s01), mul_f16x2(f[2], s23),
+                                      mul_f16x2(f[3], s23)};
+              mma_16816(o[4 * jh + j], af, pf[kt][0], pf[kt][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the stage
+      if (i + kFewStages < n_mine) {
+        const bool again = fetch(i + kFewStages);
+        present = (present & ~(1u << st)) | ((uint32_t)again << st);
+      }
     }
-  }
-  // (a wait that ran out: the error word tells; the copies still in flight land in this CTA's memory, so wait on)
-  if (!ok)
-    for (int s = 0; s < kFewStages; ++s)
-      for (int k = 0; k < 2; ++k) mbar_wait(&sm.full[warp][s], k, nullptr, 0);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
-    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
-  }
-  // join the warps: O [warp][row][channel] in the warp's own stages
-  float* po = reinterpret_cast<float*>(sm.ring[warp][0]);
-  __syncwarp();
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) po[(2 * t + (e & 1)) * DH + DH / 8 * g + 2 * j + (e >> 1)] = o[j][e];
-  if (g == 0) {
+    // (a wait that ran out: the error word tells; the copies still in flight land in this CTA's memory, so wait on)
+    if (!ok)
+      for (int s = 0; s < kFewStages; ++s)
+        for (int k = 0; k < 2; ++k) mbar_wait(&sm.full[warp][s], k, nullptr, 0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sm.m[warp][2 * t + e] = m[e];
-      sm.l[warp][2 * t + e] = l[e];
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nr * (DH / 2); i += 32 * kFewWarps) {
-    const int row = i / (DH / 2), ch = i % (DH / 2) * 2;
-    float top = sm.m[0][row];
+    // join the warps: O [warp][row][channel] in the warp's own stages
+    float* po = reinterpret_cast<float*>(sm.ring[warp][0]);
+    __syncwarp();
 #pragma unroll
-    for (int w = 1; w < kFewWarps; ++w) top = max_nan(top, sm.m[w][row]);
-    float den = 0.f, v0 = 0.f, v1 = 0.f;
-    if (top != -INFINITY) {
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        const float f = fast_exp2(sm.m[w][row] - top);
-        const float2 x = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sm.ring[w][0]) + row * DH + ch);
-        den += f * sm.l[w][row];
-        v0 += f * x.x;
-        v1 += f * x.y;
+      for (int e = 0; e < 4; ++e) po[(2 * t + (e & 1)) * DH + DH / 8 * g + 2 * j + (e >> 1)] = o[j][e];
+    if (g == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sm.m[warp][2 * t + e] = m[e];
+        sm.l[warp][2 * t + e] = l[e];
       }
-      v0 /= den;
-      v1 /= den;
     }
-    const int r = r0 + row, j = r / G, h = head * G + r % G;
-    const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(den);
-    if (a.n_splits == 1) {
-      T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
-      *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0, v1);
-      if (a.lse && ch == 0) a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
-    } else {
-      const size_t at = (((size_t)split * c.n_seq + seq) * a.rows + j) * a.n_q + h;
-      *reinterpret_cast<float2*>(static_cast<float*>(a.part_o) + at * DH + ch) = make_float2(v0, v1);
-      if (ch == 0) a.part_lse[at] = lse2;
+    __syncthreads();
+    for (int i = threadIdx.x; i < nr * (DH / 2); i += 32 * kFewWarps) {
+      const int row = i / (DH / 2), ch = i % (DH / 2) * 2;
+      float top = sm.m[0][row];
+#pragma unroll
+      for (int w = 1; w < kFewWarps; ++w) top = max_nan(top, sm.m[w][row]);
+      float den = 0.f, v0 = 0.f, v1 = 0.f;
+      if (top != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+          const float f = fast_exp2(sm.m[w][row] - top);
+          const float2 x = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(sm.ring[w][0]) + row * DH + ch);
+          den += f * sm.l[w][row];
+          v0 += f * x.x;
+          v1 += f * x.y;
+        }
+        v0 /= den;
+        v1 /= den;
+      }
+      const int r = r0 + row, j = r / G, h = head * G + r % G;
+      const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(den);
+      if (pc.whole()) {
+        T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
+        *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0, v1);
+        if (a.lse && ch == 0) a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
+      } else {
+        const size_t at = slot_of(pc) * kKv4FewTile + row;
+        *reinterpret_cast<float2*>(static_cast<float*>(a.part_o) + at * DH + ch) = make_float2(v0, v1);
+        if (ch == 0) a.part_lse[at] = lse2;
+      }
     }
+    if (!__syncthreads_and(ok)) break;   // (the rings are free again; a warp that gave up has told)
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // joining the splits: one warp for each (sequence, row, head)
 // ---------------------------------------------------------------------------------------------
-// Each split left its normalised row and base-2 log-sum-exp; the row is their mean with weights 2^(lse_s - max).
-template <int DH, typename T, typename P>
+// Each piece left its normalised row and base-2 log-sum-exp; the row is their mean with weights 2^(lse - max).  The
+// pieces of a unit are those of the CTAs whose stretches meet it: the first CTA's last piece, then first pieces.
+template <int DH, int TILE, int STEP, typename T, typename P>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
   pdl_trigger();
   pdl_wait();
   constexpr int kPer = DH / 32;
   const int lane = threadIdx.x & 31;
+  const int G = a.n_q / c.n_kv;
   const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
   const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (at >= rows) return;
   const int h = (int)(at % a.n_q), j = (int)(at / a.n_q % a.rows), seq = (int)(at / a.n_q / a.rows);
-  const int n = a.n_rows ? a.n_rows[seq] : a.rows;
-  if (j >= n || n > a.rows) return;
+  const SeqView v = seq_view(c, a, seq);
+  if (j >= v.n) return;
+  const SeqWork<TILE, STEP> w(v, G);
+  const int r = j * G + h % G;
+  const long long share = reinterpret_cast<const LineHeader*>(a.line)->share;
+  const long long start = line_base(a.line)[seq] + ((long long)(h / G) * w.tiles + r / TILE) * w.cost;
+  const int c0 = (int)(start / share), c1 = (int)((start + w.cost - 1) / share);
+  if (c0 == c1) return;   // one piece: already written
+  const size_t row = r % TILE;
+  const size_t first = 2 * (size_t)c0 + (start % share ? 1 : 0);
+  auto slot = [&](int cta) { return (cta == c0 ? first : 2 * (size_t)cta) * TILE + row; };
   float top = -INFINITY;
-  for (int s = lane; s < a.n_splits; s += 32) top = max_nan(top, a.part_lse[s * rows + at]);
+  for (int s = c0 + lane; s <= c1; s += 32) top = max_nan(top, a.part_lse[slot(s)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   float acc[kPer], den = 0.f;
@@ -378,28 +370,25 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   if (top != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < a.n_splits; ++s) {
-      const float w = fast_exp2(a.part_lse[s * rows + at] - top);
-      const P* src = static_cast<const P*>(a.part_o) + (s * rows + at) * DH + lane * kPer;
-      float v[kPer];
-      if constexpr (sizeof(P) == 4) {
+    for (int s = c0; s <= c1; ++s) {
+      const float f = fast_exp2(a.part_lse[slot(s)] - top);
+      const P* src = static_cast<const P*>(a.part_o) + slot(s) * DH + lane * kPer;
+      float x[kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(src + e);
-          v[e] = x.x;
-          v[e + 1] = x.y;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(src + e);
-          v[e] = Half<P>::lo(x);
-          v[e + 1] = Half<P>::hi(x);
+      for (int e = 0; e < kPer; e += 2) {
+        if constexpr (sizeof(P) == 4) {
+          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          x[e] = y.x;
+          x[e + 1] = y.y;
+        } else {
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(src + e);
+          x[e] = Half<P>::lo(y);
+          x[e + 1] = Half<P>::hi(y);
         }
       }
-      den += w;
+      den += f;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += w * v[e];
+      for (int e = 0; e < kPer; ++e) acc[e] += f * x[e];
     }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -418,17 +407,16 @@ cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(FewSmem<DH>));
     if (e != cudaSuccess) return e;
   }
-  const int tiles = (a.rows * (a.n_q / c.n_kv) + kKv4FewRows - 1) / kKv4FewRows;
-  return launch_k(kv4_attend_few_kernel<DH, T>, dim3(tiles, a.n_splits, c.n_seq * c.n_kv), dim3(32 * kFewWarps),
-                  sizeof(FewSmem<DH>), st, 1, c, layer, a);
+  return launch_k(kv4_attend_few_kernel<DH, T>, dim3(a.n_ctas), dim3(32 * kFewWarps), sizeof(FewSmem<DH>), st, 1, c,
+                  layer, a);
 }
 
-template <int DH, typename P>
+template <int DH, int TILE, int STEP, typename P>
 cudaError_t launch_merge(const Kv4View& c, const Kv4Attn& a, cudaStream_t st) {
   const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
   const dim3 grid((unsigned)((rows + 7) / 8));
-  return a.fp16 ? launch_k(kv4_merge_kernel<DH, __half, P>, grid, dim3(256), 0, st, 1, c, a)
-                : launch_k(kv4_merge_kernel<DH, __nv_bfloat16, P>, grid, dim3(256), 0, st, 1, c, a);
+  return a.fp16 ? launch_k(kv4_merge_kernel<DH, TILE, STEP, __half, P>, grid, dim3(256), 0, st, 1, c, a)
+                : launch_k(kv4_merge_kernel<DH, TILE, STEP, __nv_bfloat16, P>, grid, dim3(256), 0, st, 1, c, a);
 }
 
 }  // namespace
@@ -439,9 +427,12 @@ cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaSt
   return a.fp16 ? launch_few<64, __half>(c, layer, a, st) : launch_few<64, __nv_bfloat16>(c, layer, a, st);
 }
 
-cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool part_fp32, cudaStream_t st) {
-  if (c.dh == 128) return part_fp32 ? launch_merge<128, float>(c, a, st) : launch_merge<128, __half>(c, a, st);
-  return part_fp32 ? launch_merge<64, float>(c, a, st) : launch_merge<64, __half>(c, a, st);
+cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st) {
+  if (c.dh == 128)
+    return few ? launch_merge<128, kKv4FewTile, kKv4FewStep, float>(c, a, st)
+               : launch_merge<128, kKv4ManyTile, kKv4ManyStep, __half>(c, a, st);
+  return few ? launch_merge<64, kKv4FewTile, kKv4FewStep, float>(c, a, st)
+             : launch_merge<64, kKv4ManyTile, kKv4ManyStep, __half>(c, a, st);
 }
 
 }  // namespace dg

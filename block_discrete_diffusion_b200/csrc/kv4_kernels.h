@@ -46,14 +46,20 @@ struct Kv4Attn {
   long long q_seq, q_row, q_head, o_seq, o_row, o_head;
   int n_q, rows, causal, fp16;
   float scale;
-  int n_splits;
-  void* part_o;            // [n_splits][n_seq][rows][n_q][dh] (fp32 or fp16, by the form)
-  float* part_lse;         // [n_splits][n_seq][rows][n_q], base 2
+  int n_ctas;              // CTAs among which the work is divided
+  int min_share;           // key steps that a CTA takes at least
+  void* line;              // header of the division: 16 bytes and n_seq words of 8 bytes
+  void* part_o;            // [2 n_ctas][rows of a tile][dh], normalised; fp32 (few rows) or fp16
+  float* part_lse;         // [2 n_ctas][rows of a tile], base 2
 };
 
-constexpr int kKv4FewRows = 8;    // query rows of one tile of the few-rows form (one n-tile of an m16n8k16)
+// Few rows of a KV head (single tokens): tiles of 8 rows, steps of one page, mma.sync on fragments dequantised in
+// registers.  Many rows (canvases, prompt chunks): tiles of 256 rows, steps of two pages, tcgen05.
+constexpr int kKv4FewTile = 8, kKv4FewStep = 64;
+constexpr int kKv4ManyTile = 256, kKv4ManyStep = 128;
 cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
-cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool part_fp32, cudaStream_t st);
+cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
+cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st);
 
 // kernel attributes are per device: true the first time `done` (one per kernel) meets the current device
 bool first_on_device(unsigned long long* done);

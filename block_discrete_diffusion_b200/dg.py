@@ -81,7 +81,7 @@ class dg_kv4_rows(ctypes.Structure):
 class dg_kv4_attn(ctypes.Structure):
     _fields_ = [("q", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("d_rows", c_void_p)] + [
         (n, c_int64) for n in ("q_seq", "q_row", "q_head", "o_seq", "o_row", "o_head")] + [
-        (n, c_int) for n in ("n_q", "rows", "dtype", "causal")] + [("scale", c_float), ("plan_len", c_int)]
+        (n, c_int) for n in ("n_q", "rows", "dtype", "causal")] + [("scale", c_float)]
 
 
 def sampler_params(vocab, seed=0, canvas_len=256, max_steps=48, fixed_steps=0, t_start=0.8, t_end=0.4,
@@ -484,8 +484,7 @@ def dg_kv4_attend_workspace_bytes(cache: Kv4Cache, n_q, rows) -> int:
     return int(lib().dg_kv4_attend_workspace_bytes(cache.ref, n_q, rows))
 
 
-def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale=None, causal=False, plan_len=0,
-                  stream=None):
+def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale=None, causal=False, stream=None):
     """q, out [n_seq, T, n_q, d_head] (any strides with contiguous channels), lse fp32 [n_seq, T, n_q]; scale defaults to
     d_head^-0.5; rows as in dg_kv4_append."""
     c = cache.c
@@ -501,7 +500,7 @@ def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale
         raise ValueError(f"ws: expected a buffer on {cache.device}")
     a = dg_kv4_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
                     _kv4_ints(cache, rows, c.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],
-                    shape[1], code, int(bool(causal)), c.d_head ** -0.5 if scale is None else scale, plan_len)
+                    shape[1], code, int(bool(causal)), c.d_head ** -0.5 if scale is None else scale)
     _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), _ptr(ws),
                                                 ws.numel() * ws.element_size(), _kv4_stream(cache, stream)))
 

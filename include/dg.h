@@ -344,8 +344,8 @@ dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, vo
  * a single token).  A row that sees nothing is 0 with lse -inf.  Query head h reads KV head h / (n_q / n_kv).
  * Element (s, j, h, c) of q lies at q_seq * s + q_row * j + q_head * h + c elements (strides multiples of 8, rows
  * 16-byte aligned), out likewise; both of type dtype.  lse (nullable): fp32 [n_seq][rows][n_q], the natural
- * logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  plan_len: the longest length
- * to plan the key splits for (0: max_pages * 64); any length is computed right.  NaN and infinities: stale
+ * logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The
+ * work is divided among the SMs on the device, by the lengths that it finds there.  NaN and infinities: stale
  * contents behind a sequence's end never matter; a NaN among its cached values reaches every row of the call that
  * reads that page, also rows that the causal mask keeps from that position. */
 typedef struct {
@@ -356,7 +356,6 @@ typedef struct {
   int64_t q_seq, q_row, q_head, o_seq, o_row, o_head;
   int n_q, rows, dtype, causal;
   float scale;
-  int plan_len;
 } dg_kv4_attn;
 
 /* ws: device scratch, used by one call at a time. */

@@ -96,7 +96,7 @@ def check(c, layer, q, out, lse, rows, causal, scale, before=None):
         assert (d <= delta[seen] + 2.0 ** -22 * np.abs(want_lse[seen])).all(), (s, float(d.max()))
 
 
-def attend(c, n_q, T, dtype, rows=None, causal=False, seed=1, layer=0, scale=None, q_scale=1.0, plan_len=0):
+def attend(c, n_q, T, dtype, rows=None, causal=False, seed=1, layer=0, scale=None, q_scale=1.0):
     g = torch.Generator(device="cuda").manual_seed(seed)
     k = c.c
     q = (torch.randn((k.n_seq, T, n_q, k.d_head), generator=g, device="cuda") * q_scale).to(dtype)
@@ -104,8 +104,7 @@ def attend(c, n_q, T, dtype, rows=None, causal=False, seed=1, layer=0, scale=Non
     before = out.clone()
     lse = torch.full((k.n_seq, T, n_q), 7.0, device="cuda")
     ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, n_q, T), dtype=torch.uint8, device="cuda")
-    dg.dg_kv4_attend(c, layer, q, out, ws, rows=None if rows is None else dev(rows), lse=lse, causal=causal, scale=scale,
-                     plan_len=plan_len)
+    dg.dg_kv4_attend(c, layer, q, out, ws, rows=None if rows is None else dev(rows), lse=lse, causal=causal, scale=scale)
     assert dg.dg_kv4_error(c) == 0
     check(c, layer, q, out, lse, rows or [T] * k.n_seq, causal, scale or k.d_head ** -0.5, before)
     return q, out, lse
@@ -130,10 +129,8 @@ def test_rows(lens, T, rows, causal, n_q, n_kv, dh, dtype):
 
 
 @pytest.mark.parametrize("T", [1, 9, 200])
-def test_long_ragged_lengths_and_few_pages_planned(T):
-    c = make(2, 128, [9000, 70, 4097])
-    attend(c, 4, T, BF16, causal=True)
-    attend(c, 4, T, BF16, causal=True, plan_len=64)
+def test_long_ragged_lengths(T):
+    attend(make(2, 128, [9000, 70, 4097]), 4, T, BF16, causal=True)
 
 
 @pytest.mark.parametrize("q_scale,dtype", [(1e-30, BF16), (1e30, BF16), (1e-5, FP16), (500.0, FP16), (0.0, BF16)])
@@ -173,7 +170,7 @@ def test_pages_beyond_4_gib():
         for cc in (c, small):
             out = torch.empty_like(q)
             ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(cc, 16, T), dtype=torch.uint8, device="cuda")
-            dg.dg_kv4_attend(cc, 0, q, out, ws, plan_len=150)
+            dg.dg_kv4_attend(cc, 0, q, out, ws)
             outs.append(out)
         assert torch.equal(*outs)
 

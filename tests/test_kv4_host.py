@@ -88,7 +88,7 @@ def test_buffers_refused(lib):
         setattr(c, name, v)
         r = ctypes.byref(c)
         rows = dg.dg_kv4_rows(4096, 4096, 128, 128, 64, 128, 128, 64, None, 1, 0)
-        attn = dg.dg_kv4_attn(4096, 4096, None, None, 256, 256, 64, 256, 256, 64, 4, 1, 0, 0, 1.0, 0)
+        attn = dg.dg_kv4_attn(4096, 4096, None, None, 256, 256, 64, 256, 256, 64, 4, 1, 0, 0, 1.0)
         code = ctypes.c_int()
         for got in (lib.dg_kv4_init(r, None), lib.dg_kv4_extend(r, 4096, None), lib.dg_kv4_fork(r, 4096, 4096, 1, None),
                     lib.dg_kv4_free(r, 4096, 1, None), lib.dg_kv4_compact(r, None),
@@ -123,11 +123,11 @@ def test_rows_refused(lib, kw):
 
 @pytest.mark.parametrize("kw", [dict(q=None), dict(out=4104), dict(q_row=12), dict(o_seq=1), dict(n_q=3), dict(n_q=0),
                                 dict(rows=0), dict(rows=65537), dict(dtype=5), dict(causal=2), dict(scale=0.0),
-                                dict(scale=float("nan")), dict(scale=float("inf")), dict(plan_len=-1), dict(layer=2),
+                                dict(scale=float("nan")), dict(scale=float("inf")), dict(layer=2),
                                 dict(ws=None), dict(ws_bytes=10)])
 def test_attend_refused(lib, kw):
     a = dict(q=4096, out=4096, lse=None, d_rows=None, q_seq=256, q_row=256, q_head=64, o_seq=256, o_row=256, o_head=64,
-             n_q=4, rows=1, dtype=0, causal=0, scale=1.0, plan_len=0)
+             n_q=4, rows=1, dtype=0, causal=0, scale=1.0)
     a.update({k: v for k, v in kw.items() if k in a})
     attn = dg.dg_kv4_attn(*a.values())
     want = dg.DG_ERR_CAPACITY if "ws" in kw or "ws_bytes" in kw else dg.DG_ERR_INVALID_ARG

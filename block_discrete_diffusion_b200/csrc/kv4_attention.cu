@@ -12,22 +12,15 @@ namespace dg {
 
 namespace {
 
-// bytes [src, src + bytes) of global memory to shared memory, counted on bar
-__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 
@@ -66,10 +59,10 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   pdl_wait();
 
   const int G = a.n_q / c.n_kv;
-  Stretch stretch = find_stretch<kKv4FewTile, kKv4FewStep, 32 * kFewWarps>(c, a);
+  Stretch<kKv4FewTile, kKv4FewStep> stretch(c, a, blockIdx.x == 0 && warp == 0);
   Piece pc;
   int phase = 0;                // copies that each stage of the ring has seen, one bit each: its barrier's parity
-  while (next_piece<kKv4FewTile, kKv4FewStep>(c, a, stretch, pc)) {
+  while (stretch.next(pc)) {
     const int seq = pc.seq, head = pc.head;
     const SeqView sv = pc.v;
     const int r0 = pc.tile * kKv4FewTile;         // row r of the group: query row r / G, head r % G of the group
@@ -170,31 +163,43 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         const uint8_t* block = sm.ring[warp][st];
         float s[4][4];
 #pragma unroll
+        for (int kt = 0; kt < 4; ++kt) s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
+        uint32_t sw[4];   // scales of positions g and g + 8 of each tile, kH blocks each
+#pragma unroll
         for (int kt = 0; kt < 4; ++kt) {
-          s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
-          // scales of positions g and g + 8 of the tile, kH blocks each
           const uint8_t* sc = block + F::kSk + lane * 8 * F::kH + 2 * kt * F::kH;
-          const uint32_t sw = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
+          sw[kt] = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(sc) : *reinterpret_cast<const uint16_t*>(sc);
+        }
+        // the four tiles side by side: four independent chains of products
 #pragma unroll
-          for (int jh = 0; jh < F::kH; ++jh) {
+        for (int jh = 0; jh < F::kH; ++jh) {
+          uint32_t w[4][4];
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) {
             const uint4 q = *reinterpret_cast<const uint4*>(block + ((kt * F::kH + jh) * 32 + lane) * 16);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-            uint32_t s0, s1;
-            if constexpr (F::kH == 2) {
-              s0 = jh ? scale_pair<1, 1>(sw) : scale_pair<0, 0>(sw);
-              s1 = jh ? scale_pair<3, 3>(sw) : scale_pair<2, 2>(sw);
-            } else {
-              s0 = scale_pair<0, 0>(sw);
-              s1 = scale_pair<1, 1>(sw);
-            }
+            w[kt][0] = q.x;
+            w[kt][1] = q.y;
+            w[kt][2] = q.z;
+            w[kt][3] = q.w;
+          }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+              uint32_t s0, s1;
+              if constexpr (F::kH == 2) {
+                s0 = jh ? scale_pair<1, 1>(sw[kt]) : scale_pair<0, 0>(sw[kt]);
+                s1 = jh ? scale_pair<3, 3>(sw[kt]) : scale_pair<2, 2>(sw[kt]);
+              } else {
+                s0 = scale_pair<0, 0>(sw[kt]);
+                s1 = scale_pair<1, 1>(sw[kt]);
+              }
               uint32_t f[4];
-              e2m1_to_f16(w[j], f);
-              const uint32_t af[4] = {mul_f16x2(f[0], s0), mul_f16x2(f[1], s1), mul_f16x2(f[2], s0), mul_f16x2(f[3], s1)};
+              e2m1_to_f16(w[kt][j], f);
+              const uint32_t af[4] = {mul_f16x2(f[0], s0), mul_f16x2(f[1], s1), mul_f16x2(f[2], s0),
+                                      mul_f16x2(f[3], s1)};
               mma_16816(s[kt], af, qf[4 * jh + j][0], qf[4 * jh + j][1]);
             }
-          }
         }
         // base-2 scores, masked; the block's row maxima over the positions (lanes with the same t)
         float top[2] = {-INFINITY, -INFINITY};
@@ -339,8 +344,27 @@ __global__ void __launch_bounds__(32 * kFewWarps)
 // ---------------------------------------------------------------------------------------------
 // Each piece left its normalised row and base-2 log-sum-exp; the row is their mean with weights 2^(lse - max).  The
 // pieces of a unit are those of the CTAs whose stretches meet it: the first CTA's last piece, then first pieces.
-template <int DH, int TILE, int STEP, typename T, typename P>
-__global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
+struct Pieces {
+  int c0, c1;      // CTAs; one alone has written the row out itself
+  size_t first;    // slot of CTA c0's piece
+  __device__ __forceinline__ size_t slot(int cta) const { return cta == c0 ? first : 2 * (size_t)cta; }
+};
+template <int TILE, int STEP>
+__device__ __forceinline__ Pieces pieces_of(const Kv4View& c, const Kv4Attn& a, int seq, const SeqView& v, int head,
+                                            int tile) {
+  const SeqWork<TILE, STEP> w(v, a.n_q / c.n_kv);
+  const long long share = reinterpret_cast<const LineHeader*>(a.line)->share;
+  const long long start = line_base(a.line)[seq] + ((long long)head * w.tiles + tile) * w.cost;
+  Pieces p;
+  p.c0 = (int)line_div(start, share);
+  p.c1 = (int)line_div(start + w.cost - 1, share);
+  p.first = 2 * (size_t)p.c0 + (start != p.c0 * share ? 1 : 0);
+  return p;
+}
+
+// few rows: one warp for each (sequence, row, head)
+template <int DH, typename T>
+__global__ void __launch_bounds__(256) kv4_merge_few_kernel(Kv4View c, Kv4Attn a) {
   pdl_trigger();
   pdl_wait();
   constexpr int kPer = DH / 32;
@@ -352,17 +376,12 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
   const int h = (int)(at % a.n_q), j = (int)(at / a.n_q % a.rows), seq = (int)(at / a.n_q / a.rows);
   const SeqView v = seq_view(c, a, seq);
   if (j >= v.n) return;
-  const SeqWork<TILE, STEP> w(v, G);
   const int r = j * G + h % G;
-  const long long share = reinterpret_cast<const LineHeader*>(a.line)->share;
-  const long long start = line_base(a.line)[seq] + ((long long)(h / G) * w.tiles + r / TILE) * w.cost;
-  const int c0 = (int)(start / share), c1 = (int)((start + w.cost - 1) / share);
-  if (c0 == c1) return;   // one piece: already written
-  const size_t row = r % TILE;
-  const size_t first = 2 * (size_t)c0 + (start % share ? 1 : 0);
-  auto slot = [&](int cta) { return (cta == c0 ? first : 2 * (size_t)cta) * TILE + row; };
+  const Pieces p = pieces_of<kKv4FewTile, kKv4FewStep>(c, a, seq, v, h / G, r / kKv4FewTile);
+  if (p.c0 == p.c1) return;
+  const size_t row = r % kKv4FewTile;
   float top = -INFINITY;
-  for (int s = c0 + lane; s <= c1; s += 32) top = max_nan(top, a.part_lse[slot(s)]);
+  for (int s = p.c0 + lane; s <= p.c1; s += 32) top = max_nan(top, a.part_lse[p.slot(s) * kKv4FewTile + row]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   float acc[kPer], den = 0.f;
@@ -370,25 +389,17 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   if (top != -INFINITY) {
 #pragma unroll 4
-    for (int s = c0; s <= c1; ++s) {
-      const float f = fast_exp2(a.part_lse[slot(s)] - top);
-      const P* src = static_cast<const P*>(a.part_o) + slot(s) * DH + lane * kPer;
-      float x[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        if constexpr (sizeof(P) == 4) {
-          const float2 y = *reinterpret_cast<const float2*>(src + e);
-          x[e] = y.x;
-          x[e + 1] = y.y;
-        } else {
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(src + e);
-          x[e] = Half<P>::lo(y);
-          x[e + 1] = Half<P>::hi(y);
-        }
-      }
+    for (int s = p.c0; s <= p.c1; ++s) {
+      const size_t slot = p.slot(s) * kKv4FewTile + row;
+      const float f = fast_exp2(a.part_lse[slot] - top);
+      const float* src = static_cast<const float*>(a.part_o) + slot * DH + lane * kPer;
       den += f;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += f * x[e];
+      for (int e = 0; e < kPer; e += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + e);
+        acc[e] += f * y.x;
+        acc[e + 1] += f * y.y;
+      }
     }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -397,6 +408,59 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4View c, Kv4Attn a) {
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = Half<T>::pack(acc[e] * inv, acc[e + 1] * inv);
   if (a.lse && lane == 0) a.lse[at] = (top + log2f(den)) * 0.6931471805599453f;
+}
+
+// many rows: a CTA for 64 group rows of a (sequence, KV head); thread = (row, pair of 8-channel chunks): loads of the
+// same chunk by neighbouring rows are contiguous
+constexpr int kMergeRows = 64;
+template <int DH, typename T>
+__global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4View c, Kv4Attn a) {
+  pdl_trigger();
+  pdl_wait();
+  const int G = a.n_q / c.n_kv;
+  const int seq = blockIdx.z, head = blockIdx.y;
+  const SeqView v = seq_view(c, a, seq);
+  const int r = blockIdx.x * kMergeRows + threadIdx.x % kMergeRows, chunk = threadIdx.x / kMergeRows * 2;
+  if (r >= v.n * G) return;
+  const Pieces p = pieces_of<kKv4ManyTile, kKv4ManyStep>(c, a, seq, v, head, r / kKv4ManyTile);
+  if (p.c0 == p.c1) return;
+  const size_t row = r % kKv4ManyTile;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int s = p.c0; s <= p.c1; ++s) top = max_nan(top, a.part_lse[p.slot(s) * kKv4ManyTile + row]);
+  float acc[16], den = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  if (top != -INFINITY) {
+#pragma unroll 4
+    for (int s = p.c0; s <= p.c1; ++s) {
+      const size_t slot = p.slot(s);
+      const float f = fast_exp2(a.part_lse[slot * kKv4ManyTile + row] - top);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.part_o) + slot * kKv4ManyTile * DH) +
+                         chunk * kKv4ManyTile + row;
+      den += f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 y = src[u * kKv4ManyTile];
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[8 * u + 2 * e] += f * Half<__half>::lo(w[e]);
+          acc[8 * u + 2 * e + 1] += f * Half<__half>::hi(w[e]);
+        }
+      }
+    }
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int j = r / G, h = head * G + r % G;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * 8);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    dst[u] = make_uint4(Half<T>::pack(acc[8 * u] * inv, acc[8 * u + 1] * inv),
+                        Half<T>::pack(acc[8 * u + 2] * inv, acc[8 * u + 3] * inv),
+                        Half<T>::pack(acc[8 * u + 4] * inv, acc[8 * u + 5] * inv),
+                        Half<T>::pack(acc[8 * u + 6] * inv, acc[8 * u + 7] * inv));
+  if (a.lse && chunk == 0) a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = (top + log2f(den)) * 0.6931471805599453f;
 }
 
 template <int DH, typename T>
@@ -411,12 +475,14 @@ cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream
                   layer, a);
 }
 
-template <int DH, int TILE, int STEP, typename P>
-cudaError_t launch_merge(const Kv4View& c, const Kv4Attn& a, cudaStream_t st) {
-  const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
-  const dim3 grid((unsigned)((rows + 7) / 8));
-  return a.fp16 ? launch_k(kv4_merge_kernel<DH, TILE, STEP, __half, P>, grid, dim3(256), 0, st, 1, c, a)
-                : launch_k(kv4_merge_kernel<DH, TILE, STEP, __nv_bfloat16, P>, grid, dim3(256), 0, st, 1, c, a);
+template <int DH, typename T>
+cudaError_t launch_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st) {
+  if (few) {
+    const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
+    return launch_k(kv4_merge_few_kernel<DH, T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, c, a);
+  }
+  const dim3 grid((a.rows * (a.n_q / c.n_kv) + kMergeRows - 1) / kMergeRows, c.n_kv, c.n_seq);
+  return launch_k(kv4_merge_many_kernel<DH, T>, grid, dim3(kMergeRows * DH / 16), 0, st, 1, c, a);
 }
 
 }  // namespace
@@ -429,10 +495,8 @@ cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaSt
 
 cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st) {
   if (c.dh == 128)
-    return few ? launch_merge<128, kKv4FewTile, kKv4FewStep, float>(c, a, st)
-               : launch_merge<128, kKv4ManyTile, kKv4ManyStep, __half>(c, a, st);
-  return few ? launch_merge<64, kKv4FewTile, kKv4FewStep, float>(c, a, st)
-             : launch_merge<64, kKv4ManyTile, kKv4ManyStep, __half>(c, a, st);
+    return a.fp16 ? launch_merge<128, __half>(c, a, few, st) : launch_merge<128, __nv_bfloat16>(c, a, few, st);
+  return a.fp16 ? launch_merge<64, __half>(c, a, few, st) : launch_merge<64, __nv_bfloat16>(c, a, few, st);
 }
 
 }  // namespace dg

@@ -18,6 +18,24 @@ struct SeqView {
   int len, n;   // positions, query rows
 };
 
+// a / b and a % b of line positions (64-bit division only where 32 bits do not do: it is a long routine)
+__device__ __forceinline__ long long line_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// mbar_wait by a whole warp, which leaves it together: the lanes see a phase end at different polls, and what
+// follows (tcgen05.ld and .st, products) must be reached by all of them at once.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, DEV_ERR_TIMEOUT_ATTN));
+}
+
+// bytes [src, src + bytes) of global memory to shared memory, counted on bar
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // A sequence's length and row count; nothing to do for one whose counts do not fit (each kernel reports them once).
 __device__ __forceinline__ SeqView seq_view(const Kv4View& c, const Kv4Attn& a, int seq, bool report = false) {
   SeqView v;
@@ -48,47 +66,13 @@ struct SeqWork {
   __device__ __forceinline__ long long total(int n_kv) const { return (long long)tiles * n_kv * cost; }
 };
 
-// A CTA's stretch of the line: `left` steps from step `step` of unit `unit` of sequence `seq` on.
-struct Stretch {
-  long long left;
-  int seq, unit, step;
-  bool at_begin;   // the next piece is the stretch's first
-};
-
 // One piece: steps [s0, s1) of a unit of `cost` steps.
 struct Piece {
   SeqView v;
   int seq, head, tile, s0, s1, cost;
-  bool first;
+  bool first;   // the first of its CTA's stretch
   __device__ __forceinline__ bool whole() const { return s0 == 0 && s1 == cost; }
 };
-
-template <int TILE, int STEP>
-__device__ __forceinline__ bool next_piece(const Kv4View& c, const Kv4Attn& a, Stretch& st, Piece& p) {
-  const int G = a.n_q / c.n_kv;
-  while (st.left > 0 && st.seq < c.n_seq) {
-    p.v = seq_view(c, a, st.seq);
-    const SeqWork<TILE, STEP> w(p.v, G);
-    if (st.unit >= w.tiles * c.n_kv) {
-      ++st.seq;
-      st.unit = st.step = 0;
-      continue;
-    }
-    p.seq = st.seq;
-    p.head = st.unit / w.tiles;
-    p.tile = st.unit % w.tiles;
-    p.cost = w.cost;
-    p.s0 = st.step;
-    p.s1 = (int)min((long long)w.cost, st.step + st.left);
-    p.first = st.at_begin;
-    st.at_begin = false;
-    st.left -= p.s1 - p.s0;
-    st.step = 0;
-    ++st.unit;
-    return true;
-  }
-  return false;
-}
 
 // Line header in the workspace, for the merge kernel: base[s] is the line position of sequence s's first unit.
 struct LineHeader {
@@ -98,68 +82,104 @@ __host__ __device__ __forceinline__ long long* line_base(void* line) {
   return reinterpret_cast<long long*>(line) + 2;
 }
 
-// Whole CTA of NT threads (a multiple of 32): this CTA's stretch.  CTA 0 also leaves the line's header.
-template <int TILE, int STEP, int NT>
-__device__ Stretch find_stretch(const Kv4View& c, const Kv4Attn& a) {
-  __shared__ long long warp_sums[NT / 32];
-  __shared__ Stretch found;
-  const int G = a.n_q / c.n_kv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool lead = blockIdx.x == 0;
-  auto cost = [&](int s) {
-    if (s >= c.n_seq) return 0ll;
-    return SeqWork<TILE, STEP>(seq_view(c, a, s, lead), G).total(c.n_kv);
-  };
-  // exclusive prefix over the CTA's threads, and their total
-  auto scan = [&](long long v, long long& total) {
+// A CTA's stretch of the line, walked piece by piece.  Each warp walks it for itself, without shared memory or
+// barriers: lane l holds the counts of sequence 32 w + l of the current window, so a window costs one round of loads.
+template <int TILE, int STEP>
+struct Stretch {
+  const Kv4View& c;
+  const Kv4Attn& a;
+  int G, lane;
+  SeqView mine;            // counts of sequence window + lane
+  int window;
+  long long left;          // steps that the stretch still has
+  int seq, unit, step;     // where it goes on
+  bool at_begin;
+
+  __device__ __forceinline__ void load(int w, bool report = false) {
+    window = w;
+    mine = SeqView{0, 0};
+    if (w + lane < c.n_seq) mine = seq_view(c, a, w + lane, report);
+  }
+  __device__ __forceinline__ long long cost_of_mine() const {
+    return SeqWork<TILE, STEP>(mine, G).total(c.n_kv);
+  }
+  // exclusive prefix of v over the lanes; the sum in `total`
+  __device__ __forceinline__ long long scan(long long v, long long& total) const {
     long long s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long u = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += u;
     }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = s;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) before += warp_sums[w];
-      total += warp_sums[w];
-    }
-    return before + s - v;
-  };
-  long long total = 0, part, mine = 0, at = 0;
-  for (int s0 = 0; s0 < c.n_seq; s0 += NT) {
-    mine = cost(s0 + threadIdx.x);
-    at = total + scan(mine, part);
-    total += part;
-    if (lead && s0 + (int)threadIdx.x < c.n_seq) line_base(a.line)[s0 + threadIdx.x] = at;
+    total = __shfl_sync(0xffffffffu, s, 31);
+    return s - v;
   }
-  const long long share = max((long long)a.min_share, (total + gridDim.x - 1) / gridDim.x);
-  const long long begin = share * blockIdx.x;
-  if (lead && threadIdx.x == 0) reinterpret_cast<LineHeader*>(a.line)->share = share;
-  if (threadIdx.x == 0) found = Stretch{0, c.n_seq, 0, 0, true};
-  __syncthreads();
-  if (begin < total) {
+
+  // Whole warp.  `lead`: the one warp of the grid that leaves the header and reports counts that do not fit.
+  __device__ __forceinline__ Stretch(const Kv4View& c_, const Kv4Attn& a_, bool lead)
+      : c(c_), a(a_), G(a_.n_q / c_.n_kv), lane(threadIdx.x & 31), left(0), seq(c_.n_seq), unit(0), step(0),
+        at_begin(true) {
+    long long total = 0, part, at = 0;
+#pragma unroll 1
+    for (int w = 0; w < c.n_seq; w += 32) {
+      load(w, lead);
+      at = total + scan(cost_of_mine(), part);
+      total += part;
+      if (lead && w + lane < c.n_seq) line_base(a.line)[w + lane] = at;
+    }
+    const long long share = max((long long)a.min_share, line_div(total + gridDim.x - 1, gridDim.x));
+    const long long begin = share * blockIdx.x;
+    if (lead && lane == 0) reinterpret_cast<LineHeader*>(a.line)->share = share;
+    if (begin >= total) return;
+    left = min(share, total - begin);
     long long base = 0;
-    for (int s0 = 0; s0 < c.n_seq; s0 += NT) {
-      if (c.n_seq > NT) {   // (else `mine` and `at` still hold the only round)
-        mine = cost(s0 + threadIdx.x);
-        at = base + scan(mine, part);
+#pragma unroll 1
+    for (int w = 0; w < c.n_seq; w += 32) {
+      if (c.n_seq > 32) {   // (else `mine` and `at` still hold the only window)
+        load(w);
+        at = base + scan(cost_of_mine(), part);
         base += part;
       }
-      if (mine > 0 && at <= begin && begin < at + mine) {
-        const int s = s0 + threadIdx.x;
-        const SeqWork<TILE, STEP> w(seq_view(c, a, s), G);
-        found = Stretch{min(share, total - begin), s, (int)((begin - at) / w.cost), (int)((begin - at) % w.cost), true};
+      const uint32_t hit = __ballot_sync(0xffffffffu, at <= begin && begin < at + cost_of_mine());
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const long long off = begin - __shfl_sync(0xffffffffu, at, l);
+        const int cost = max(1, (__shfl_sync(0xffffffffu, mine.len, l) + STEP - 1) / STEP);
+        seq = w + l;
+        unit = (int)line_div(off, cost);
+        step = (int)(off - (long long)unit * cost);
+        return;
       }
     }
   }
-  __syncthreads();
-  return found;
-}
+
+  __device__ __forceinline__ bool next(Piece& p) {
+    while (left > 0 && seq < c.n_seq) {
+      if (seq >= window + 32) load(seq & ~31);
+      p.v.len = __shfl_sync(0xffffffffu, mine.len, seq & 31);
+      p.v.n = __shfl_sync(0xffffffffu, mine.n, seq & 31);
+      const SeqWork<TILE, STEP> w(p.v, G);
+      if (unit >= w.tiles * c.n_kv) {
+        ++seq;
+        unit = step = 0;
+        continue;
+      }
+      p.seq = seq;
+      p.head = unit / w.tiles;
+      p.tile = unit % w.tiles;
+      p.cost = w.cost;
+      p.s0 = step;
+      p.s1 = (int)min((long long)w.cost, step + left);
+      p.first = at_begin;
+      at_begin = false;
+      left -= p.s1 - p.s0;
+      step = 0;
+      ++unit;
+      return true;
+    }
+    return false;
+  }
+};
 
 // the workspace slot of a piece that is part of a unit
 __device__ __forceinline__ size_t slot_of(const Piece& p) { return 2 * (size_t)blockIdx.x + (p.first ? 0 : 1); }

@@ -1,13 +1,21 @@
 // kv4_canvas.cu -- attention over the paged 4-bit cache for many rows: canvases and prompt chunks, on tcgen05.
 //
-// A CTA works on 256 rows of a KV head (two 128-row tiles) and steps of 128 positions (two pages), so each dequantised
-// step serves 256 rows.  Warp roles (416 threads):
-//   warps 0-3    softmax of tile 0, warps 4-7 softmax of tile 1 (thread = row): the row of Q into shared memory, S from
-//                TMEM, P = 2^(S - m) in fp16 to shared memory, running sum, the finished row out
-//   warps 8-11   dequantise: codes and scales from global memory into registers, one step ahead; fp16 K and V tiles
-//                in the 128-byte swizzled layout of the tensor core, through a ring of three buffers
-//   warp 12      issues the products: S_x = Q_x K^T and O_x += P_x V in the order
-//                S_0(0) S_1(0) | PV_0(t) S_0(t+1) PV_1(t) S_1(t+1) ..., one tile's products under the other's softmax
+// A CTA works on 256 rows of a KV head (two 128-row tiles) and steps of one page, so each dequantised page serves
+// 256 rows.  Warp roles (512 threads):
+//   warps 0-3    softmax of tile 0, warps 4-7 softmax of tile 1 (thread = row): Q into shared memory, S from TMEM,
+//                P = 2^(S - m) in fp16 back into S's columns of TMEM, running sum, the finished row out
+//   warps 8-11   dequantise: pages' blocks from a ring of three in shared memory to fp16 K and V tiles in the 128-byte
+//                swizzled layout of the tensor core, a ring of eight
+//   warp 12      issues the products of tile 0, warp 15 those of tile 1: S = Q K^T of a step, O += P V of the step two before
+//   warp 13      walks the CTA's stretch and hands its pieces to the others, up to four ahead
+//   warp 14      copies the pages' blocks into their ring, one bulk copy each
+//
+// Two S of 64 columns a tile fill TMEM beside the two O, so while a tile's exponentials of one step run, its next S is
+// there already and the tensor core works on the other products; with one S of 128 columns each tile waited for its
+// products and then they for it (5000 cycles for 128 positions, of which 2200 of products and 2050 of exponentials).
+// P as the tensor core's operand in TMEM and not in shared memory takes 128 KB off the 384 KB that 128 positions
+// cost there; the blocks come by bulk copies because loads into registers were waited for by each tile's proxy fence.
+//
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
 // positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in the same
 // order, which only renames registers.  The running maximum is lazy: O and the sum are rescaled when a row's
@@ -20,20 +28,37 @@ namespace dg {
 
 namespace {
 
-constexpr int kManyThreads = 416;
-constexpr int kRing = 3;
+constexpr int kManyThreads = 512;
+// Registers a thread after the split of the launch's 4 x 128: two softmax groups, the dequantisers, the issuers.
+constexpr int kRegsSoftmax = 152, kRegsDequant = 120, kRegsIssue = 88;
+static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * 128, "register split above what the CTA was launched with");
+constexpr int kRing = 8;       // fp16 tiles of 64 positions
+constexpr int kRaw = 3;        // pages' blocks
 constexpr float kLazy = 8.f;   // log2 units
 
 template <int DH>
 struct ManySmem {
-  static constexpr uint32_t kTile = 128u * DH * 2u;   // a Q, K or V tile
-  static constexpr uint32_t kP = 128u * 128u * 2u;
-  static constexpr size_t kBytes = 1024 + 2 * kTile + kRing * kTile + 2 * kP + 256;
+  static constexpr uint32_t kQ = 128u * DH * 2u;       // a Q tile
+  static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
+  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640;
+  static_assert(kBytes <= 232448, "shared memory budget");
 };
 
+// A piece of work as the roles need it.
+struct Task {
+  int seq, head, row0, nr;      // its rows: [row0, row0 + nr) of the sequence's group rows
+  int s0, steps;                // its pages that some row sees: [s0, s0 + steps); steps < 0: no more pieces
+  int len, n, whole, slot;
+};
+constexpr int kTasks = 4;
+constexpr int kTaskReaders = 15;   // warps that read a task
+
 struct ManyBars {
-  uint64_t q_full[2], s_full[2], s_free[2], p_ready[2], pv_done[2];
-  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t task_full[kTasks], task_empty[kTasks];
+  Task task[kTasks];
+  uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2][2];   // by tile, by S buffer
+  uint64_t kv_full[kRing], kv_empty[kRing], raw_full[kRaw], raw_empty[kRaw];
+  int raw_there[kRaw];   // 0: the page is behind the sequence's end (or not one): its values count as zeros
   uint32_t tmem;
 };
 
@@ -65,17 +90,50 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 32 columns of packed words to this warp's lanes
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t* r) {
+  tmem_st32(taddr, reinterpret_cast<const float*>(r));
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, 16-bit inputs, fp32 accumulate; one thread issues.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive without release semantics: for tensor memory, whose accesses tcgen05.wait and tcgen05.fence order.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // kind::f16 with fp16 operands, fp32 accumulators, both K-major
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// steps of 128 positions that the rows of a piece have to look at, within [s0, s1)
-__device__ __forceinline__ int piece_steps(const Piece& p, int G, int causal, int& nr) {
-  nr = (int)min((long long)kKv4ManyTile, (long long)p.v.n * G - (long long)p.tile * kKv4ManyTile);
-  const int limit = row_limit(p.v, (p.tile * kKv4ManyTile + nr - 1) / G, causal);
-  return max(0, min((limit + kKv4ManyStep - 1) / kKv4ManyStep, p.s1) - p.s0);
-}
+// The reading end of the tasks, one for each warp.
+struct Tasks {
+  ManyBars* bars;
+  int* err;
+  uint32_t i = 0;
+  __device__ __forceinline__ bool next(Task& t) {   // whole warp
+    const int k = i % kTasks;
+    if (!warp_wait(&bars->task_full[k], (i / kTasks) & 1, err)) return false;
+    t = bars->task[k];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->task_empty[k]);
+    ++i;
+    return t.steps >= 0;
+  }
+};
 
 template <int DH, typename T>
 __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4View c, int layer, Kv4Attn a) {
@@ -84,27 +142,37 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = base;
-  uint8_t* kv_s = q_s + 2 * C::kTile;
-  uint8_t* p_s = kv_s + kRing * C::kTile;
-  ManyBars* bars = reinterpret_cast<ManyBars*>(p_s + 2 * C::kP);
+  uint8_t* kv_s = q_s + 2 * C::kQ;
+  uint8_t* raw_s = kv_s + kRing * C::kTile;
+  ManyBars* bars = reinterpret_cast<ManyBars*>(raw_s + kRaw * F::kBytes);
+  static_assert(sizeof(ManyBars) <= 640, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = c.head + KV4_WORD_WAIT;
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->q_full[x], 4);
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->s_free[x], 4);
-      mbar_init(&bars->p_ready[x], 4);
-      mbar_init(&bars->pv_done[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[x][b], 1);
+        mbar_init(&bars->pv_done[x][b], 1);
+        mbar_init(&bars->p_ready[x][b], 4);
+      }
     }
     for (int b = 0; b < kRing; ++b) {
       mbar_init(&bars->kv_full[b], 4);
-      mbar_init(&bars->kv_empty[b], 1);
+      mbar_init(&bars->kv_empty[b], 2);   // both issuers
+    }
+    for (int k = 0; k < kRaw; ++k) {
+      mbar_init(&bars->raw_full[k], 1);
+      mbar_init(&bars->raw_empty[k], 4);
+    }
+    for (int k = 0; k < kTasks; ++k) {
+      mbar_init(&bars->task_full[k], 1);
+      mbar_init(&bars->task_empty[k], kTaskReaders);
     }
     fence_mbar_init();
   }
-  if (warp == 12) tmem_alloc(&bars->tmem, 512);   // S_0 [0,128) S_1 [128,256) O_0 [256,..) O_1 [384,..)
+  if (warp == 12) tmem_alloc(&bars->tmem, 512);   // tile x: S [128 x, +64) and [128 x + 64, +64), O [256 + 128 x, ..)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -112,112 +180,92 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   pdl_wait();
 
   const int G = a.n_q / c.n_kv;
-  Stretch stretch = find_stretch<kKv4ManyTile, kKv4ManyStep, kManyThreads>(c, a);
-  Piece pc;
+  Tasks tasks{bars, err};
+  Task pc;
   bool ok = true;
 
   if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
     // ------------------------------ dequantise ------------------------------
+    // K: warp w takes the page's 16-position tile w.  V: tiles 2 hv + {0, 1} with hv = (w & 1) ^ (g & 1), so that the lanes of
+    // a store meet different banks, and half w >> 1 of a lane's channels.
     const int w = warp - 8, g = lane >> 2, t = lane & 3;
-    const int pg = w >> 1;                       // this warp's page of a step
-    uint32_t item = 0;                           // K and V tiles laid down so far
-    while (next_piece<kKv4ManyTile, kKv4ManyStep>(c, a, stretch, pc)) {
-      int nr;
-      const int steps = piece_steps(pc, G, a.causal, nr);
-      const int n_pages = (pc.v.len + kPage - 1) / kPage;
-      const int32_t* table = c.table + (size_t)pc.seq * c.max_pages;
-      const uint8_t* plane = c.pool + ((size_t)layer * c.n_pages * c.n_kv + pc.head) * F::kBytes;
-      // this warp's page of step i, or null
-      int ids = -1;
-      auto block_of = [&](int i) -> const uint8_t* {   // whole warp, i ascending
-        if ((i & 31) == 0) {
-          const int page = 2 * (pc.s0 + i + lane) + pg;
-          ids = i + lane < steps && page < n_pages ? table[page] : -1;
-          if (i + lane < steps && page < n_pages && (ids < 0 || ids >= c.n_pages)) {
-            report_error(c.head, DEV_ERR_BAD_INDEX);
-            ids = -1;
+    const int hv = (w & 1) ^ (g & 1);
+    uint32_t item = 0, page = 0;                 // K and V tiles laid down, pages read so far
+    while (tasks.next(pc)) {
+      for (int i = 0; i < pc.steps; ++i, ++page) {
+        const int left = pc.len - (pc.s0 + i) * kPage;   // positions of this page that exist
+        const uint32_t slot = page % kRaw;
+        ok = ok && warp_wait(&bars->raw_full[slot], (page / kRaw) & 1, err);
+        const uint8_t* blk = raw_s + slot * F::kBytes;
+        const bool there = ok && bars->raw_there[slot];
+        uint4 k[F::kH];
+        uint32_t v[2][2 * F::kH], ks, vs[2];
+        {
+          const uint8_t* s = blk + F::kSk + lane * 8 * F::kH + 2 * w * F::kH;
+          ks = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(s) : *reinterpret_cast<const uint16_t*>(s);
+#pragma unroll
+          for (int jh = 0; jh < F::kH; ++jh) {
+            // (lanes t 2 and 3 take the channel halves in the other order, for the banks)
+            const int jk = F::kH == 2 ? jh ^ (t >> 1) : 0;
+            k[jh] = *reinterpret_cast<const uint4*>(blk + ((w * F::kH + jk) * 32 + lane) * 16);
           }
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-        return id < 0 ? nullptr : plane + (size_t)id * c.n_kv * F::kBytes;
-      };
-      // K: 16-position tiles 2 (w & 1) + {0, 1}; V: tiles 2 h + {0, 1} with h = (w & 1) ^ (g & 1), so that the lanes of
-      // a store meet different banks
-      const int hv = (w & 1) ^ (g & 1);
-      uint4 ck[2][F::kH], cv[2][F::kH];
-      uint32_t sk[2], sv[2];
-      auto load = [&](const uint8_t* blk) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int kt = 2 * (w & 1) + u, vt = 2 * hv + u;
-          sk[u] = sv[u] = 0;
-#pragma unroll
-          for (int jh = 0; jh < F::kH; ++jh) ck[u][jh] = cv[u][jh] = make_uint4(0, 0, 0, 0);
-          if (blk) {
-            const uint8_t* s = blk + F::kSk + lane * 8 * F::kH + 2 * kt * F::kH;
-            sk[u] = F::kH == 2 ? *reinterpret_cast<const uint32_t*>(s) : *reinterpret_cast<const uint16_t*>(s);
-            sv[u] = *reinterpret_cast<const uint32_t*>(blk + F::kSv + ((F::kH == 2 ? g : g >> 1) * 4 + t) * 16 + 4 * vt);
-#pragma unroll
-            for (int jh = 0; jh < F::kH; ++jh) {
-              // (K: lanes t 2 and 3 take the channel halves in the other order, for the banks)
-              const int jk = F::kH == 2 ? jh ^ (t >> 1) : 0;
-              ck[u][jh] = *reinterpret_cast<const uint4*>(blk + ((kt * F::kH + jk) * 32 + lane) * 16);
-              cv[u][jh] = *reinterpret_cast<const uint4*>(blk + F::kV + ((vt * F::kH + jh) * 32 + lane) * 16);
+          for (int u = 0; u < 2; ++u) {
+            const int vt = 2 * hv + u;
+            vs[u] = *reinterpret_cast<const uint32_t*>(blk + F::kSv + ((F::kH == 2 ? g : g >> 1) * 4 + t) * 16 + 4 * vt);
+            if constexpr (F::kH == 2) {
+              const uint4 q = *reinterpret_cast<const uint4*>(blk + F::kV + ((vt * 2 + (w >> 1)) * 32 + lane) * 16);
+              v[u][0] = q.x;
+              v[u][1] = q.y;
+              v[u][2] = q.z;
+              v[u][3] = q.w;
+            } else {
+              const uint2 q = *reinterpret_cast<const uint2*>(blk + F::kV + (vt * 32 + lane) * 16 + 8 * (w >> 1));
+              v[u][0] = q.x;
+              v[u][1] = q.y;
             }
           }
         }
-      };
-      if (steps > 0) load(block_of(0));
-      for (int i = 0; i < steps; ++i) {
-        uint4 k[2][F::kH], v[2][F::kH];
-        uint32_t ks[2], vs[2];
-        const int left = pc.v.len - (pc.s0 + i) * kKv4ManyStep - pg * kPage;   // positions of this page that exist
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->raw_empty[slot]);   // (the block is in registers)
+        // a page that is not there: code 0 at scale 0 for all
+        if (!there) {
+          ks = vs[0] = vs[1] = 0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          ks[u] = sk[u];
-          vs[u] = sv[u];
-#pragma unroll
-          for (int jh = 0; jh < F::kH; ++jh) {
-            k[u][jh] = ck[u][jh];
-            v[u][jh] = cv[u][jh];
-          }
+          for (int jh = 0; jh < F::kH; ++jh) k[jh] = make_uint4(0, 0, 0, 0);
         }
-        if (i + 1 < steps) load(block_of(i + 1));
         // ---- K ----
         {
           const int b = item % kRing;
-          ok = ok && mbar_wait(&bars->kv_empty[b], ((item / kRing) & 1) ^ 1, err, DEV_ERR_TIMEOUT_ATTN);
-          uint8_t* dst = kv_s + (size_t)b * C::kTile;
+          ok = ok && warp_wait(&bars->kv_empty[b], ((item / kRing) & 1) ^ 1, err);
+          const int row = 16 * w + g;   // and row + 8
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int row = pg * kPage + 16 * (2 * (w & 1) + u) + g;   // and row + 8
+          for (int jh = 0; jh < F::kH; ++jh) {
+            const int jk = F::kH == 2 ? jh ^ (t >> 1) : 0;
+            uint32_t s0, s1;
+            if constexpr (F::kH == 2) {
+              const uint32_t two = jk ? ks >> 8 : ks;
+              s0 = scale_pair<0, 0>(two);
+              s1 = scale_pair<2, 2>(two);
+            } else {
+              s0 = scale_pair<0, 0>(ks);
+              s1 = scale_pair<1, 1>(ks);
+            }
+            const uint32_t wd[4] = {k[jh].x, k[jh].y, k[jh].z, k[jh].w};
+            const int plane64 = F::kH == 2 ? t >> 1 : 0;
+            const int chunk0 = F::kH == 2 ? (t & 1) * 4 + 2 * jk : 2 * t;
+            uint8_t* rp = kv_s + (size_t)b * C::kTile + plane64 * 8192 + row * 128;
 #pragma unroll
-            for (int jh = 0; jh < F::kH; ++jh) {
-              const int jk = F::kH == 2 ? jh ^ (t >> 1) : 0;
-              uint32_t s0, s1;
-              if constexpr (F::kH == 2) {
-                const uint32_t two = jk ? ks[u] >> 8 : ks[u];
-                s0 = scale_pair<0, 0>(two);
-                s1 = scale_pair<2, 2>(two);
-              } else {
-                s0 = scale_pair<0, 0>(ks[u]);
-                s1 = scale_pair<1, 1>(ks[u]);
-              }
-              const uint32_t wd[4] = {k[u][jh].x, k[u][jh].y, k[u][jh].z, k[u][jh].w};
-              const int plane64 = F::kH == 2 ? t >> 1 : 0;
-              const int chunk0 = F::kH == 2 ? (t & 1) * 4 + 2 * jk : 2 * t;
-              uint8_t* rp = dst + plane64 * 16384 + row * 128;
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                uint32_t f0[4], f1[4];
-                e2m1_to_f16(wd[2 * q], f0);
-                e2m1_to_f16(wd[2 * q + 1], f1);
-                const int off = ((chunk0 + q) ^ (row & 7)) << 4;   // (row + 8 has the same swizzle)
-                *reinterpret_cast<uint4*>(rp + off) = make_uint4(mul_f16x2(f0[0], s0), mul_f16x2(f0[2], s0),
-                                                                mul_f16x2(f1[0], s0), mul_f16x2(f1[2], s0));
-                *reinterpret_cast<uint4*>(rp + 1024 + off) = make_uint4(mul_f16x2(f0[1], s1), mul_f16x2(f0[3], s1),
-                                                                       mul_f16x2(f1[1], s1), mul_f16x2(f1[3], s1));
-              }
+            for (int q = 0; q < 2; ++q) {
+              uint32_t f0[4], f1[4];
+              e2m1_to_f16(wd[2 * q], f0);
+              e2m1_to_f16(wd[2 * q + 1], f1);
+              const int off = ((chunk0 + q) ^ g) << 4;   // (row and row + 8 have the same swizzle)
+              *reinterpret_cast<uint4*>(rp + off) = make_uint4(mul_f16x2(f0[0], s0), mul_f16x2(f0[2], s0),
+                                                              mul_f16x2(f1[0], s0), mul_f16x2(f1[2], s0));
+              *reinterpret_cast<uint4*>(rp + 1024 + off) = make_uint4(mul_f16x2(f0[1], s1), mul_f16x2(f0[3], s1),
+                                                                     mul_f16x2(f1[1], s1), mul_f16x2(f1[3], s1));
             }
           }
           fence_proxy_async_smem();
@@ -228,8 +276,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         // ---- V ----
         {
           const int b = item % kRing;
-          ok = ok && mbar_wait(&bars->kv_empty[b], ((item / kRing) & 1) ^ 1, err, DEV_ERR_TIMEOUT_ATTN);
-          uint8_t* dst = kv_s + (size_t)b * C::kTile + pg * (DH * 128);
+          ok = ok && warp_wait(&bars->kv_empty[b], ((item / kRing) & 1) ^ 1, err);
+          uint8_t* dst = kv_s + (size_t)b * C::kTile;
           uint32_t s01[2], s23[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -244,22 +292,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
             s23[u] = scale_pair<2, 3>(vs[u]);
           }
           const int chunk = 2 * t + hv;
+          const int ch0 = DH / 8 * g + DH / 16 * (w >> 1);   // first channel (a multiple of 4 or 8)
 #pragma unroll
-          for (int jh = 0; jh < F::kH; ++jh) {
-            const uint32_t w0[4] = {v[0][jh].x, v[0][jh].y, v[0][jh].z, v[0][jh].w};
-            const uint32_t w1[4] = {v[1][jh].x, v[1][jh].y, v[1][jh].z, v[1][jh].w};
+          for (int j = 0; j < 2 * F::kH; ++j) {
+            uint32_t f0[4], f1[4];
+            e2m1_to_f16(v[0][j], f0);
+            e2m1_to_f16(v[1][j], f1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t f0[4], f1[4];
-              e2m1_to_f16(w0[j], f0);
-              e2m1_to_f16(w1[j], f1);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int ch = DH / 8 * g + 8 * jh + 2 * j + e;
-                *reinterpret_cast<uint4*>(dst + ch * 128 + ((chunk ^ ((2 * j + e) & 7)) << 4)) =
-                    make_uint4(mul_f16x2(f0[e], s01[0]), mul_f16x2(f0[2 + e], s23[0]), mul_f16x2(f1[e], s01[1]),
-                               mul_f16x2(f1[2 + e], s23[1]));
-              }
+            for (int e = 0; e < 2; ++e) {
+              const int ch = ch0 + 2 * j + e;
+              *reinterpret_cast<uint4*>(dst + ch * 128 + ((chunk ^ (ch & 7)) << 4)) =
+                  make_uint4(mul_f16x2(f0[e], s01[0]), mul_f16x2(f0[2 + e], s23[0]), mul_f16x2(f1[e], s01[1]),
+                             mul_f16x2(f1[2 + e], s23[1]));
             }
           }
           fence_proxy_async_smem();
@@ -269,192 +313,222 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         }
       }
     }
-  } else if (warp == 12) {
-    // ------------------------------ products ------------------------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(128, 128);
-      constexpr uint32_t idesc_o = idesc_f16_f32(128, DH);
-      uint32_t item = 0, n_tile[2] = {0, 0}, n_piece[2] = {0, 0};   // items used, steps of each tile, pieces of each tile
-      while (next_piece<kKv4ManyTile, kKv4ManyStep>(c, a, stretch, pc)) {
-        int nr;
-        const int steps = piece_steps(pc, G, a.causal, nr);
-        if (steps == 0) continue;   // (nothing to see: the softmax warps write the rows without any product)
-        const int nx = nr > 128 ? 2 : 1;
-        for (int x = 0; x < nx; ++x) {
-          ok = ok && mbar_wait(&bars->q_full[x], n_piece[x] & 1, err, DEV_ERR_TIMEOUT_ATTN);
-          ++n_piece[x];
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 13) {
+      // ------------------------------ pieces ------------------------------
+      Stretch<kKv4ManyTile, kKv4ManyStep> stretch(c, a, blockIdx.x == 0);
+      Piece p;
+      for (uint32_t i = 0;; ++i) {
+        const int k = i % kTasks;
+        const bool more = stretch.next(p);
+        if (!warp_wait(&bars->task_empty[k], ((i / kTasks) & 1) ^ 1, err)) break;
+        if (lane == 0) {
+          Task t{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
+          if (more) {
+            const int row0 = p.tile * kKv4ManyTile, nr = min(kKv4ManyTile, p.v.n * G - row0);
+            const int limit = row_limit(p.v, (row0 + nr - 1) / G, a.causal);   // the last row sees the most
+            const int steps = max(0, min((limit + kKv4ManyStep - 1) / kKv4ManyStep, p.s1) - p.s0);
+            t = Task{p.seq, p.head, row0, nr, p.s0, steps, p.v.len, p.v.n, p.whole(), (int)slot_of(p)};
+          }
+          bars->task[k] = t;
+          mbar_arrive(&bars->task_full[k]);
         }
-        auto issue_s = [&](int x, int i) {
-          const uint32_t it = item + 2 * i, b = it % kRing;
-          ok = ok && mbar_wait(&bars->kv_full[b], (it / kRing) & 1, err, DEV_ERR_TIMEOUT_ATTN);
-          ok = ok && mbar_wait(&bars->s_free[x], ((n_tile[x] + i) & 1) ^ 1, err, DEV_ERR_TIMEOUT_ATTN);
-          tc_fence_after();
-          if (ok) {
-            const uint8_t* kb = kv_s + (size_t)b * C::kTile;
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-              const uint64_t ad =
-                  desc_advance(smem_desc_sw128(smem_u32(q_s + x * C::kTile + (kk / 4) * 16384)), (kk % 4) * 32);
-              const uint64_t bd = desc_advance(smem_desc_sw128(smem_u32(kb + (kk / 4) * 16384)), (kk % 4) * 32);
-              umma_bf16(tmem + x * 128, ad, bd, idesc_s, kk != 0);
+        __syncwarp();
+        if (!more) break;
+      }
+    } else if (warp == 14) {
+      // ------------------------------ blocks ------------------------------
+      uint32_t page = 0;
+      while (tasks.next(pc) && ok) {
+        const int32_t* table = c.table + (size_t)pc.seq * c.max_pages;
+        const uint8_t* plane = c.pool + ((size_t)layer * c.n_pages * c.n_kv + pc.head) * F::kBytes;
+        int ids = -1;   // 32 pages' ids at a time, one a lane
+        for (int i = 0; i < pc.steps && ok; ++i, ++page) {
+          if ((i & 31) == 0) {
+            const bool wanted = i + lane < pc.steps;   // (the steps end at the last page that a row sees)
+            ids = wanted ? table[pc.s0 + i + lane] : -1;
+            if (wanted && (ids < 0 || ids >= c.n_pages)) {
+              report_error(c.head, DEV_ERR_BAD_INDEX);
+              ids = -1;
             }
           }
-          umma_commit(&bars->s_full[x]);
-          if (x == nx - 1) umma_commit(&bars->kv_empty[b]);
-        };
-        auto issue_pv = [&](int x, int i) {
-          const uint32_t it = item + 2 * i + 1, b = it % kRing;
-          ok = ok && mbar_wait(&bars->kv_full[b], (it / kRing) & 1, err, DEV_ERR_TIMEOUT_ATTN);
-          ok = ok && mbar_wait(&bars->p_ready[x], (n_tile[x] + i) & 1, err, DEV_ERR_TIMEOUT_ATTN);
-          tc_fence_after();
-          if (ok) {
-            const uint8_t* vb = kv_s + (size_t)b * C::kTile;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint64_t ad =
-                  desc_advance(smem_desc_sw128(smem_u32(p_s + x * C::kP + (kk / 4) * 16384)), (kk % 4) * 32);
-              const uint64_t bd = desc_advance(smem_desc_sw128(smem_u32(vb + (kk / 4) * (DH * 128))), (kk % 4) * 32);
-              umma_bf16(tmem + 256 + x * 128, ad, bd, idesc_o, (i | kk) != 0);
+          const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+          const uint32_t slot = page % kRaw;
+          ok = warp_wait(&bars->raw_empty[slot], ((page / kRaw) & 1) ^ 1, err);
+          if (ok && lane == 0) {
+            bars->raw_there[slot] = id >= 0;
+            if (id >= 0) {
+              mbar_arrive_expect_tx(&bars->raw_full[slot], F::kBytes);
+              bulk_load(&bars->raw_full[slot], raw_s + slot * F::kBytes, plane + (size_t)id * c.n_kv * F::kBytes,
+                        F::kBytes);
+            } else {
+              mbar_arrive(&bars->raw_full[slot]);
             }
           }
-          umma_commit(&bars->pv_done[x]);
-          if (x == nx - 1) umma_commit(&bars->kv_empty[b]);
-        };
-        for (int x = 0; x < nx; ++x) issue_s(x, 0);
-        for (int i = 0; i < steps; ++i)
-          for (int x = 0; x < nx; ++x) {
-            issue_pv(x, i);
-            if (i + 1 < steps) issue_s(x, i + 1);
+          __syncwarp();
+        }
+      }
+      // (after a wait that ran out: copies still in flight land in this CTA's memory)
+      if (!ok)
+        for (int k = 0; k < 2 * kRaw; ++k) mbar_wait(&bars->raw_full[k / 2], k & 1, nullptr, 0);
+    } else {
+      // ------------------------------ products of tile x ------------------------------
+      // (the whole warp waits, lane 0 issues)
+      const int x = warp == 12 ? 0 : 1;
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, 64);
+      constexpr uint32_t idesc_o = idesc_f16_f32(128, DH);
+      // low words of the operands' descriptors (start address / 16; a shared-memory address fits the field)
+      const uint32_t q_lo = (smem_u32(q_s + x * C::kQ) >> 4) | 1u << 16, kv_lo = (smem_u32(kv_s) >> 4) | 1u << 16;
+      const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0) >> 32);
+      auto desc_of = [&](uint32_t lo) { return (uint64_t)desc_hi << 32 | lo; };
+      const uint32_t t_s = tmem + x * 128, t_o = tmem + 256 + x * 128;
+      uint32_t item = 0, n_step = 0, n_piece = 0;   // K and V tiles of all pieces; steps and pieces of this tile
+      auto full = [&](uint32_t it) {
+        ok = ok && warp_wait(&bars->kv_full[it % kRing], (it / kRing) & 1, err);
+      };
+      while (tasks.next(pc)) {
+        const int steps = pc.steps;
+        if (steps == 0) continue;   // (nothing to see: the softmax warps write the rows without any product)
+        if (x * 128 >= pc.nr) {     // no rows in this tile: let the buffers go
+          for (int i = 0; i < 2 * steps; ++i, ++item) {
+            full(item);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->kv_empty[item % kRing]);
           }
+          continue;
+        }
+        ok = ok && warp_wait(&bars->q_full[x], n_piece++ & 1, err);
+        // S of step h, from K tile item + 2 h, into buffer (n_step of h) & 1.  Its columns are free: S there was read
+        // before P took their place, and P there was multiplied before (products complete in order)
+        auto issue_s = [&](int h, uint32_t buf) {
+          const uint32_t b = (item + 2 * h) % kRing;
+          full(item + 2 * h);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t bd = kv_lo + b * (C::kTile >> 4);
+            if (ok) {
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk)
+                umma_bf16(t_s + 64 * buf, desc_of(q_lo + (kk / 4) * (16384 >> 4) + (kk % 4) * 2),
+                          desc_of(bd + (kk / 4) * (8192 >> 4) + (kk % 4) * 2), idesc_s, kk != 0);
+            }
+            umma_commit(&bars->s_full[x][buf]);
+            umma_commit(&bars->kv_empty[b]);
+          }
+          __syncwarp();
+        };
+        issue_s(0, n_step & 1);
+        if (steps > 1) issue_s(1, (n_step & 1) ^ 1);
+        for (int i = 0; i < steps; ++i, ++n_step) {
+          const uint32_t it = item + 2 * i + 1, b = it % kRing, buf = n_step & 1;
+          full(it);
+          ok = ok && warp_wait(&bars->p_ready[x][buf], (n_step >> 1) & 1, err);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t bd = kv_lo + b * (C::kTile >> 4);
+            if (ok) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f16_ts(t_o, t_s + 64 * buf + kk * 8, desc_of(bd + kk * 2), idesc_o, (i | kk) != 0);
+            }
+            umma_commit(&bars->pv_done[x][buf]);
+            umma_commit(&bars->kv_empty[b]);
+          }
+          __syncwarp();
+          if (i + 2 < steps) issue_s(i + 2, buf);
+        }
         item += 2 * steps;
-        for (int x = 0; x < nx; ++x) n_tile[x] += steps;
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------ softmax ------------------------------
     const int x = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + x * 128;
     const uint32_t t_o = tmem + lane_off + 256 + x * 128;
-    uint8_t* prow = p_s + x * C::kP + r * 128;
-    uint8_t* qrow = q_s + x * C::kTile + r * 128;
-    uint32_t n_tile = 0;                         // steps of this tile so far
-    while (next_piece<kKv4ManyTile, kKv4ManyStep>(c, a, stretch, pc)) {
-      int nr;
-      const int steps = piece_steps(pc, G, a.causal, nr);
-      if (x * 128 >= nr) continue;               // (the issuer skips this tile too)
-      const bool valid = x * 128 + r < nr;
+    uint8_t* qtile = q_s + x * C::kQ + (warp & 3) * 32 * 128;   // this warp's 32 rows
+    uint32_t n_step = 0;                         // steps of this tile so far
+    while (tasks.next(pc)) {
+      const int steps = pc.steps;
+      if (x * 128 >= pc.nr) continue;            // (the issuer skips this tile too)
+      const bool valid = x * 128 + r < pc.nr;
       // a row behind the last one goes along with its limit, so that its warp's shortcuts hold
-      const int rr = pc.tile * kKv4ManyTile + (valid ? x * 128 + r : nr - 1);
+      const int rr = pc.row0 + (valid ? x * 128 + r : pc.nr - 1);
       const int j = rr / G, h = pc.head * G + rr % G;
-      const int limit = row_limit(pc.v, j, a.causal);
+      const int limit = row_limit(SeqView{pc.len, pc.n}, j, a.causal);
       float sl2 = 0.f;
       if (steps > 0) {
-        // Q: this thread's row to fp16 in the swizzled layout, times a power of two (the S products of the last
-        // piece, which read this row, are complete: this warp has read the last S)
-        const T* q = static_cast<const T*>(a.q) + pc.seq * a.q_seq + j * a.q_row + h * a.q_head;
-        uint4 raw[DH / 8];
-        float amax = 0.f;
+        // Q to fp16 in the swizzled layout, times a power of two: dh / 8 lanes a row, so that a row is read in one
+        // piece (the S products of the last piece, which read these rows, are complete: this warp has read the last S)
+        constexpr int kLanes = DH / 8, kRows = 32 / kLanes;
+        const int sub = lane % kLanes;
+        float mine = 0.f;
+        uint4 all[32 / kRows];
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i) {
-          raw[i] = valid ? reinterpret_cast<const uint4*>(q)[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(Half<T>::lo(wd[e])), fabsf(Half<T>::hi(wd[e]))));
+        for (int i = 0; i < 32; i += kRows) {
+          const int at = x * 128 + (warp & 3) * 32 + i + lane / kLanes, R = pc.row0 + at;
+          all[i / kRows] = make_uint4(0, 0, 0, 0);
+          if (at < pc.nr)
+            all[i / kRows] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + pc.seq * a.q_seq +
+                                                             (R / G) * a.q_row + (pc.head * G + R % G) * a.q_head + sub * 8);
         }
-        float down, up;
-        row_powers(amax, down, up);
 #pragma unroll
-        for (int i = 0; i < DH / 8; ++i) {
-          uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        for (int i = 0; i < 32; i += kRows) {
+          const int row = i + lane / kLanes;
+          const uint4 raw = all[i / kRows];
+          uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) amax = max3(amax, fabsf(Half<T>::lo(wd[e])), fabsf(Half<T>::hi(wd[e])));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float down, up;
+          row_powers(amax, down, up);
 #pragma unroll
           for (int e = 0; e < 4; ++e) wd[e] = pack_f16x2(Half<T>::lo(wd[e]) * down, Half<T>::hi(wd[e]) * down);
-          *reinterpret_cast<uint4*>(qrow + (i / 8) * 16384 + (((i & 7) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(qtile + (sub / 8) * 16384 + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
               make_uint4(wd[0], wd[1], wd[2], wd[3]);
+          const float u = __shfl_sync(0xffffffffu, up, (lane % kRows) * kLanes);   // of row i + lane % kRows
+          if (lane / kRows == i / kRows) mine = u;
         }
-        sl2 = a.scale * 1.4426950408889634f * up;
+        sl2 = fmaxf(a.scale * 1.4426950408889634f * mine, 1e-44f);   // (above 0, so that -inf stays -inf)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full[x]);
       }
       float m_used = -INFINITY, l = 0.f;
-      for (int i = 0; i < steps; ++i, ++n_tile) {
-        ok = ok && mbar_wait(&bars->s_full[x], n_tile & 1, err, DEV_ERR_TIMEOUT_ATTN);
+      for (int i = 0; i < steps; ++i, ++n_step) {
+        const uint32_t buf = n_step & 1;
+        const uint32_t t_s = tmem + lane_off + x * 128 + 64 * buf;
+        ok = ok && warp_wait(&bars->s_full[x][buf], (n_step >> 1) & 1, err);
         tc_fence_after();
         const int kmax = limit - (pc.s0 + i) * kKv4ManyStep;   // positions of this step that the row sees
-        const bool full = kmax >= kKv4ManyStep;
-        auto p_pass = [&](float m_ref, float& rmax) {
-          uint64_t lt2 = 0;
-          const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-m_ref, -m_ref);
-          rmax = -INFINITY;
+        float s[64];
+        tmem_ld32(t_s, s);
+        tmem_ld32(t_s + 32, s + 32);
+        tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, kmax >= kKv4ManyStep)) {
 #pragma unroll
-          for (int cb = 0; cb < 128; cb += 64) {
-            float s[64];
-            tmem_ld32(t_s + cb, s);
-            tmem_ld32(t_s + cb + 32, s + 32);
-            tmem_wait_ld();
-            uint32_t pk[32];
-            if (full) {
-#pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                rmax = fmaxf(rmax, fmaxf(s[e], s[e + 1]));
-                const uint64_t y = ffma_f32x2(pack_f32x2(s[e], s[e + 1]), sl2x2, negm2);
-                const float p0 = fast_exp2(lo_f32(y)), p1 = fast_exp2(hi_f32(y));
-                lt2 = fadd_f32x2(lt2, pack_f32x2(p0, p1));
-                pk[e / 2] = pack_f16x2(p0, p1);
-              }
-            } else {
-              float lt = 0.f;
-#pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                const bool v0 = cb + e < kmax, v1 = cb + e + 1 < kmax;   // masked: p = 0
-                if (v0) rmax = fmaxf(rmax, s[e]);
-                if (v1) rmax = fmaxf(rmax, s[e + 1]);
-                const float p0 = v0 ? fast_exp2(fmaf(s[e], sl2, -m_ref)) : 0.f;
-                const float p1 = v1 ? fast_exp2(fmaf(s[e + 1], sl2, -m_ref)) : 0.f;
-                lt += p0 + p1;
-                pk[e / 2] = pack_f16x2(p0, p1);
-              }
-              lt2 = fadd_f32x2(lt2, pack_f32x2(lt, 0.f));
-            }
-            // position order of V: chunk 2 t + h holds pairs t of 8-position groups 4 h .. 4 h + 3
-            uint8_t* out = prow + (cb / 64) * 16384;
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              const int at = 16 * (ch & 1) + (ch >> 1);
-              *reinterpret_cast<uint4*>(out + ((ch ^ (r & 7)) << 4)) =
-                  make_uint4(pk[at], pk[at + 4], pk[at + 8], pk[at + 12]);
-            }
-          }
-          return lo_f32(lt2) + hi_f32(lt2);
-        };
-        // PV of the step before is complete (products complete in order), so O and P are free here
-        float rmax = -INFINITY, lt = 0.f;
-        bool redo = m_used == -INFINITY;
-        if (!__any_sync(0xffffffffu, redo)) {
-          lt = p_pass(m_used, rmax);
-          redo = rmax * sl2 > m_used + kLazy;
+          for (int e = 0; e < 64; ++e) s[e] = e < kmax ? s[e] : -INFINITY;
         }
-        if (__any_sync(0xffffffffu, redo)) {
-          rmax = -INFINITY;
+        // the row's maximum (raw scores; the scale is positive)
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int cb = 0; cb < 128; cb += 64) {
-            float s[64];
-            tmem_ld32(t_s + cb, s);
-            tmem_ld32(t_s + cb + 32, s + 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (cb + e < kmax) rmax = fmaxf(rmax, s[e]);
-          }
-          const float tmax = rmax * sl2;
-          const bool grow = redo && tmax > m_used + kLazy;
+        for (int e = 0; e < 64; e += 2) top[e / 2 & 3] = max3(top[e / 2 & 3], s[e], s[e + 1]);
+        // the reference follows when the maximum has grown by more than kLazy (the first finite one: above -inf)
+        const float tmax = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sl2;
+        const bool grow = tmax > m_used + kLazy;
+        if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? tmax : m_used;
-          const float alpha = (grow && m_used != -INFINITY) ? fast_exp2(m_used - m_new) : 1.f;
+          const float alpha = grow && m_used != -INFINITY ? fast_exp2(m_used - m_new) : 1.f;
           l *= alpha;
           m_used = m_new;
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
+            // O holds the steps before this one once the last of their products is complete
+            ok = ok && warp_wait(&bars->pv_done[x][buf ^ 1], ((n_step - 1) >> 1) & 1, err);
+            tc_fence_after();
+#pragma unroll 1
             for (int cb = 0; cb < DH; cb += 32) {
               float o[32];
               tmem_ld32(t_o + cb, o);
@@ -463,31 +537,44 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
               for (int e = 0; e < 32; ++e) o[e] *= alpha;
               tmem_st32(t_o + cb, o);
             }
-            tmem_wait_st();
           }
-          lt = p_pass(m_used, rmax);
         }
-        l += lt;
-        fence_proxy_async_smem();
+        // P over S, in V's order: words 4 ch .. 4 ch + 3 (chunk ch = 2 t + b) are the pairs t of the 8-position groups
+        // 4 b .. 4 b + 3.  (Nothing seen yet: every score is -inf, p is 0.)
+        const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+        const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-m_ref, -m_ref);
+        uint64_t sum[2] = {0, 0};
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const uint64_t y = ffma_f32x2(pack_f32x2(s[e], s[e + 1]), sl2x2, negm2);
+          const float p0 = fast_exp2(lo_f32(y)), p1 = fast_exp2(hi_f32(y));
+          sum[e / 2 & 1] = fadd_f32x2(sum[e / 2 & 1], pack_f32x2(p0, p1));
+          pk[8 * (e / 2 % 4) + e / 8] = pack_f16x2(p0, p1);   // pair e / 2 = 4 group + t -> word 8 t + group
+        }
+        tmem_st32u(t_s, pk);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bars->s_free[x]);
-          mbar_arrive(&bars->p_ready[x]);
-        }
+        if (lane == 0) mbar_arrive_relaxed(&bars->p_ready[x][buf]);
+        const uint64_t both = fadd_f32x2(sum[0], sum[1]);
+        l += lo_f32(both) + hi_f32(both);
       }
       // ---- the row out ----
       if (steps > 0) {
-        ok = ok && mbar_wait(&bars->pv_done[x], (n_tile - 1) & 1, err, DEV_ERR_TIMEOUT_ATTN);
+        // (one barrier a buffer: the products of the last two steps may both be under way here)
+        ok = ok && warp_wait(&bars->pv_done[x][(n_step - 1) & 1], ((n_step - 1) >> 1) & 1, err);
         tc_fence_after();
       }
       const bool some = steps > 0 && l != 0.f;   // (a row may see nothing; a NaN sum goes through)
       const float inv = some ? 1.f / l : 0.f;
       const float lse2 = some ? m_used + log2f(l) : -INFINITY;
-      const bool whole = pc.whole();
       T* dst = static_cast<T*>(a.out) + pc.seq * a.o_seq + j * a.o_row + h * a.o_head;
-      const size_t at = slot_of(pc) * kKv4ManyTile + x * 128 + r;
-      __half* part = static_cast<__half*>(a.part_o) + at * DH;
+      const size_t at = (size_t)pc.slot * kKv4ManyTile + x * 128 + r;
+      // a part in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; 16-byte chunks of the
+      // tile's rows side by side, so that a warp's stores and the merge's loads are contiguous
+      uint4* part = reinterpret_cast<uint4*>(static_cast<__half*>(a.part_o) + (size_t)pc.slot * kKv4ManyTile * DH) +
+                    x * 128 + r;
 #pragma unroll
       for (int cb = 0; cb < DH; cb += 32) {
         float o[32];
@@ -496,24 +583,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
         if (valid && ok) {
-          if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
+          for (int e = 0; e < 32; e += 8) {
+            if (pc.whole)
               *reinterpret_cast<uint4*>(dst + cb + e) =
                   make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
                              Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
-          } else {
-            // a part in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(part + cb + e) =
+            else
+              part[(cb + e) / 8 * kKv4ManyTile] =
                   make_uint4(pack_f16x2(o[e], o[e + 1]), pack_f16x2(o[e + 2], o[e + 3]),
                              pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
           }
         }
       }
       if (valid && ok) {
-        if (!whole)
+        if (!pc.whole)
           a.part_lse[at] = lse2;
         else if (a.lse)
           a.lse[((size_t)pc.seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;

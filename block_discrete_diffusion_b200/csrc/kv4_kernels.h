@@ -49,14 +49,14 @@ struct Kv4Attn {
   int n_ctas;              // CTAs among which the work is divided
   int min_share;           // key steps that a CTA takes at least
   void* line;              // header of the division: 16 bytes and n_seq words of 8 bytes
-  void* part_o;            // [2 n_ctas][rows of a tile][dh], normalised; fp32 (few rows) or fp16
+  void* part_o;            // normalised; few rows: fp32 [2 n_ctas][tile][dh]; many: fp16 [2 n_ctas][dh / 8][tile][8]
   float* part_lse;         // [2 n_ctas][rows of a tile], base 2
 };
 
 // Few rows of a KV head (single tokens): tiles of 8 rows, steps of one page, mma.sync on fragments dequantised in
-// registers.  Many rows (canvases, prompt chunks): tiles of 256 rows, steps of two pages, tcgen05.
+// registers.  Many rows (canvases, prompt chunks): tiles of 256 rows, steps of one page, tcgen05.
 constexpr int kKv4FewTile = 8, kKv4FewStep = 64;
-constexpr int kKv4ManyTile = 256, kKv4ManyStep = 128;
+constexpr int kKv4ManyTile = 256, kKv4ManyStep = 64;
 cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st);

@@ -491,3 +491,10 @@ def test_wrong_tensors_are_refused():
         dg.dg_kv4_attend(c, 0, q, q, ws[:16])
     with pytest.raises(dg.DGError):
         dg.dg_kv4_attend(c, 1, q, q, ws)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_long_lengths_with_few_and_many_rows(causal):
+    """Sequences whose rows fill one 128-row tile, two, or part of one, long enough for many steps of each."""
+    attend(make(2, 128, [5000, 3001, 4097, 2500]), 4, 256, BF16, rows=[40, 256, 64, 65], causal=causal)
+    attend(make(1, 64, [4000, 6000]), 1, 130, FP16, rows=[129, 128], causal=causal)

@@ -92,7 +92,7 @@ int current_sms() {
 // How a call's work is divided: the form, and the CTAs among which it goes.
 struct Plan {
   bool few;
-  int n_ctas, min_share;
+  int cluster, n_ctas, min_share;
   size_t tile, row_bytes;   // rows of a workspace slot, bytes of a row in it
   size_t bytes(const dg_kv4_cache* c) const { return line_bytes(c) + 2 * (size_t)n_ctas * tile * (row_bytes + 4); }
   static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
@@ -102,11 +102,19 @@ struct Plan {
 constexpr int kFewRows = 16;
 
 Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
-  Plan p;
+  Plan p{};
   p.few = (long long)rows * (n_q / c->n_kv) <= kFewRows;
   const int sms = current_sms();
   if (p.few) {
-    p.n_ctas = sms * (c->d_head == 128 ? 2 : 4);   // what fits the SMs' shared memory at once
+    p.n_ctas = sms * (c->d_head == 128 ? 3 : 5);   // what fits the SMs' shared memory at once
+    // A cluster for each unit where the sequences cannot be long: one launch and no parts in memory (one token behind
+    // 577 positions: 11.7 -> 7.0 us).  Longer units want more warps than a cluster of such CTAs has (32768 positions:
+    // 21.2 us on the line, 24.8 in clusters of 16 CTAs, 24.3 of 12-warp CTAs that fill an SM), and units of different lengths
+    // leave SMs idle: from about 24 pages a CTA on that costs more than the second launch.
+    const long long units = ((long long)rows * (n_q / c->n_kv) + kKv4FewTile - 1) / kKv4FewTile * c->n_kv * c->n_seq;
+    int n = kKv4MaxCluster;
+    while (n > 1 && units * n > p.n_ctas) n /= 2;
+    if (units <= p.n_ctas && c->max_pages <= 24 * n) p.cluster = n;
     p.min_share = 4;                               // a page for each warp
     p.tile = kKv4FewTile;
     p.row_bytes = 4 * (size_t)c->d_head;
@@ -237,6 +245,7 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   k.causal = a->causal;
   k.fp16 = a->dtype == DG_DTYPE_FP16;
   k.scale = a->scale;
+  k.cluster = p.cluster;
   k.n_ctas = p.n_ctas;
   k.min_share = p.min_share;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
@@ -246,7 +255,7 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   const Kv4View v = view(c);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = p.few ? kv4_attend_few(v, layer, k, s) : kv4_attend_many(v, layer, k, s);
-  if (e == cudaSuccess) e = kv4_attend_merge(v, k, p.few, s);
+  if (e == cudaSuccess && !p.cluster) e = kv4_attend_merge(v, k, p.few, s);
   return launched(fn, e);
 }
 

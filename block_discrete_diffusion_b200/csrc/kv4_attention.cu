@@ -27,13 +27,18 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 // ---------------------------------------------------------------------------------------------
 // few rows: single tokens and other tiles of at most 8 rows of a KV head
 // ---------------------------------------------------------------------------------------------
+// A call of few units whose lengths cannot differ much runs a cluster for each unit, which joins its CTAs' rows through
+// distributed shared memory in the same launch; others divide the line of all units evenly (kv4_attention.cuh) and
+// join in a second launch.
+//
 // 4 warps; a warp takes every fourth page of the CTA's piece of a unit.  It keeps a ring of whole blocks in shared memory (one bulk copy each: a block is contiguous), dequantises them into
 // m16n8k16 fragments and multiplies S = K Q^T and O^T += V^T P^T: positions and channels are the 16-wide
 // side, the rows the 8-wide one, so a tile of 8 rows wastes no tensor work, and a row's statistics lie with the same
 // lanes in S and in O^T.  Bound by the cache's bytes: mma.sync is enough, since 8 rows x 2 operations a value
 // stay far below its rate.
-constexpr int kFewWarps = 4;
-constexpr int kFewStages = 3;
+constexpr int kFewWarps = 4;               // warps of a CTA; three CTAs an SM keep 24 blocks in flight
+constexpr int kFewStages = 2;
+constexpr int kMaxCluster = kKv4MaxCluster;
 
 template <int DH>
 struct FewSmem {
@@ -42,7 +47,19 @@ struct FewSmem {
   float m[kFewWarps][kKv4FewTile], l[kFewWarps][kKv4FewTile];
 };
 
-template <int DH, typename T>
+__device__ __forceinline__ float2 dsmem_ld_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float dsmem_ld_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Cluster: grid (unit, 1, CTA of the unit's cluster); else the CTAs divide the line.
+template <int DH, typename T, bool Cluster>
 __global__ void __launch_bounds__(32 * kFewWarps)
     kv4_attend_few_kernel(Kv4View c, int layer, Kv4Attn a) {
   using F = Kv4<DH>;
@@ -59,10 +76,10 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   pdl_wait();
 
   const int G = a.n_q / c.n_kv;
-  Stretch<kKv4FewTile, kKv4FewStep> stretch(c, a, blockIdx.x == 0 && warp == 0);
-  Piece pc;
   int phase = 0;                // copies that each stage of the ring has seen, one bit each: its barrier's parity
-  while (stretch.next(pc)) {
+  bool ok = true;
+  // one piece of work
+  auto work = [&](const Piece& pc) {
     const int seq = pc.seq, head = pc.head;
     const SeqView sv = pc.v;
     const int r0 = pc.tile * kKv4FewTile;         // row r of the group: query row r / G, head r % G of the group
@@ -151,7 +168,6 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     float o[NJ][4];               // O^T: channels DH/8 g + 2 j + {0, 1}, rows 2t, 2t + 1
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    bool ok = true;
     for (int i = 0; i < n_mine; ++i) {
       const int st = i % kFewStages;
       ok = ok && mbar_wait(&sm.full[warp][st], (phase >> st) & 1, c.head + KV4_WORD_WAIT, DEV_ERR_TIMEOUT_ATTN);
@@ -292,6 +308,8 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     }
     // join the warps: O [warp][row][channel] in the warp's own stages
     float* po = reinterpret_cast<float*>(sm.ring[warp][0]);
+    float* part = reinterpret_cast<float*>(sm.ring[0][1]);   // a cluster's CTA: its joined rows
+    float* part_lse = part + kKv4FewTile * DH;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -323,9 +341,12 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         v0 /= den;
         v1 /= den;
       }
-      const int r = r0 + row, j = r / G, h = head * G + r % G;
       const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(den);
-      if (pc.whole()) {
+      const int r = r0 + row, j = r / G, h = head * G + r % G;
+      if (Cluster && gridDim.z > 1) {
+        *reinterpret_cast<float2*>(part + row * DH + ch) = make_float2(v0, v1);
+        if (ch == 0) part_lse[row] = lse2;
+      } else if (pc.whole()) {
         T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
         *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0, v1);
         if (a.lse && ch == 0) a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
@@ -335,7 +356,68 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         if (ch == 0) a.part_lse[at] = lse2;
       }
     }
-    if (!__syncthreads_and(ok)) break;   // (the rings are free again; a warp that gave up has told)
+    if (Cluster && gridDim.z > 1) {
+      // every CTA of the cluster joins its share of the rows' channel pairs from all of them
+      cluster_sync();
+      const int n = gridDim.z;
+      const uint32_t o_addr = smem_u32(part), lse_addr = smem_u32(part_lse);
+      for (int i = blockIdx.z * 32 * kFewWarps + threadIdx.x; i < nr * (DH / 2); i += n * 32 * kFewWarps) {
+        const int row = i / (DH / 2), ch = i % (DH / 2) * 2;
+        float le[kMaxCluster];
+        float2 x[kMaxCluster];
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          le[k] = k < n ? dsmem_ld_f1(dsmem_map(lse_addr + 4 * row, k)) : -INFINITY;
+          x[k] = k < n ? dsmem_ld_f2(dsmem_map(o_addr + 4 * (row * DH + ch), k)) : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) top = max_nan(top, le[k]);
+        float den = 0.f, v0 = 0.f, v1 = 0.f;
+        if (top != -INFINITY) {
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            const float f = k < n ? fast_exp2(le[k] - top) : 0.f;
+            den += f;
+            v0 += f * x[k].x;
+            v1 += f * x[k].y;
+          }
+          v0 /= den;
+          v1 /= den;
+        }
+        const int r = r0 + row, j = r / G, h = head * G + r % G;
+        T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
+        *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0, v1);
+        if (a.lse && ch == 0)
+          a.lse[((size_t)seq * a.rows + j) * a.n_q + h] =
+              (top == -INFINITY ? -INFINITY : top + log2f(den)) * 0.6931471805599453f;
+      }
+      cluster_sync();   // this CTA's rows stay until all have read them
+    }
+  };
+  if constexpr (Cluster) {
+    // unit: (sequence, KV head, tile) with the tiles that `rows` rows would have
+    const int tiles = (a.rows * G + kKv4FewTile - 1) / kKv4FewTile;
+    Piece pc;
+    pc.tile = blockIdx.x % tiles;
+    pc.head = blockIdx.x / tiles % c.n_kv;
+    pc.seq = blockIdx.x / tiles / c.n_kv;
+    pc.v = seq_view(c, a, pc.seq, threadIdx.x == 0);
+    if (pc.tile * kKv4FewTile >= pc.v.n * G) return;   // (the whole cluster)
+    const int pages = (pc.v.len + kPage - 1) / kPage;
+    const int per = (pages + gridDim.z - 1) / gridDim.z;
+    pc.cost = max(1, pages);
+    pc.s0 = gridDim.z == 1 ? 0 : min(pages, (int)blockIdx.z * per);
+    pc.s1 = gridDim.z == 1 ? pc.cost : min(pages, pc.s0 + per);
+    pc.first = true;
+    work(pc);
+  } else {
+    Stretch<kKv4FewTile, kKv4FewStep> stretch(c, a, blockIdx.x == 0 && warp == 0);
+    Piece pc;
+    while (stretch.next(pc)) {
+      work(pc);
+      if (!__syncthreads_and(ok)) break;   // (the rings are free again; a warp that gave up has told)
+    }
   }
 }
 
@@ -467,12 +549,23 @@ template <int DH, typename T>
 cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st) {
   static unsigned long long done = 0;
   if (first_on_device(&done)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(FewSmem<DH>));
+    cudaError_t e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(FewSmem<DH>));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               sizeof(FewSmem<DH>));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(kv4_attend_few_kernel<DH, T>, dim3(a.n_ctas), dim3(32 * kFewWarps), sizeof(FewSmem<DH>), st, 1, c,
-                  layer, a);
+  if (a.cluster) {
+    const int units = (a.rows * (a.n_q / c.n_kv) + kKv4FewTile - 1) / kKv4FewTile * c.n_kv * c.n_seq;
+    return launch_k(kv4_attend_few_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(32 * kFewWarps),
+                    sizeof(FewSmem<DH>), st, a.cluster, c, layer, a);
+  }
+  return launch_k(kv4_attend_few_kernel<DH, T, false>, dim3(a.n_ctas), dim3(32 * kFewWarps),
+                  sizeof(FewSmem<DH>), st, 1,
+                  c, layer, a);
 }
 
 template <int DH, typename T>

@@ -361,7 +361,7 @@ class Kv4Cache:
     def __init__(self, c, pool, book):
         self.c, self.pool, self.book = c, pool, book
         self.ref = ctypes.byref(c)
-        self.device = pool.device
+        self.device, self.index = pool.device, pool.device.index
         pad = lambda n: (n + 3) // 4 * 4   # noqa: E731
         refs = 16 + pad(c.n_seq)
         table = refs + pad(c.n_pages)
@@ -403,18 +403,25 @@ def dg_kv4_book_bytes(c) -> int:
     return int(lib().dg_kv4_book_bytes(ctypes.byref(getattr(c, "c", c))))
 
 
+# the current stream's handle without building a Stream object (3 us of a call's 15)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _kv4_stream(cache, stream):
     """The stream's handle; the kernels run on the current device, so the cache has to lie there."""
-    if cache.device.index != torch.cuda.current_device():
+    if cache.index != torch.cuda.current_device():
         raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream_handle(stream)
+    if stream is None:
+        return _current_raw_stream(cache.index)
+    return stream.cuda_stream
 
 
 def _kv4_ints(cache, t, n, what):
     """An int32 argument of n values on the cache's device (None stays None)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != cache.device or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
+    if t.dtype != torch.int32 or t.get_device() != cache.index or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{what}: expected {n} contiguous int32 values on {cache.device}")
     return t.data_ptr()
 
@@ -424,7 +431,7 @@ def _kv4_tensor(cache, t, shape, what, dtype=None):
     code = _KV4_DTYPES.get(t.dtype)
     if code is None or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{what}: expected bf16 or fp16, the same for every tensor of the call")
-    if tuple(t.shape) != tuple(shape) or t.device != cache.device:
+    if t.shape != shape or t.get_device() != cache.index:
         raise ValueError(f"{what}: expected shape {tuple(shape)} on {cache.device}, got {tuple(t.shape)} on {t.device}")
     s = t.stride()
     if s[3] != 1:
@@ -493,10 +500,10 @@ def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale
     shape = (c.n_seq, q.shape[1], q.shape[2], c.d_head)
     code, qs = _kv4_tensor(cache, q, shape, "q")
     _, os_ = _kv4_tensor(cache, out, shape, "out", q.dtype)
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != shape[:3] or not lse.is_contiguous()
-                            or lse.device != cache.device):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()
+                            or lse.get_device() != cache.index):
         raise ValueError(f"lse: expected a contiguous fp32 tensor {shape[:3]} on {cache.device}")
-    if ws.device != cache.device:
+    if ws.get_device() != cache.index:
         raise ValueError(f"ws: expected a buffer on {cache.device}")
     a = dg_kv4_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
                     _kv4_ints(cache, rows, c.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],

@@ -119,6 +119,22 @@ def test_single_tokens(lens, n_q, n_kv, dh, dtype):
     attend(make(n_kv, dh, lens), n_q, 1, dtype, causal=True)
 
 
+@pytest.mark.parametrize("lens", [[1], [63, 64, 65], [700, 1, 257, 0, 513], [9000, 70, 4097], [300] * 40], ids=str)
+@pytest.mark.parametrize("n_q,n_kv,dh,dtype", [(16, 8, 128, BF16), (4, 2, 64, FP16), (8, 1, 64, BF16)])
+def test_single_tokens_that_may_have_long_contexts(lens, n_q, n_kv, dh, dtype):
+    """The same in caches whose sequences may be long: the work is divided along all sequences and its parts are joined."""
+    attend(make(n_kv, dh, lens, max_pages=3000), n_q, 1, dtype, causal=True)
+    attend(make(n_kv, dh, lens, max_pages=3000), n_q, 2, dtype, rows=[min(2, n + 1) for n in range(len(lens))])
+
+
+@pytest.mark.parametrize("n_seq", [33, 400])
+def test_many_short_sequences(n_seq):
+    lens = [(7 * i) % 90 for i in range(n_seq)]
+    attend(make(1, 64, lens), 2, 1, FP16, causal=True)
+    attend(make(1, 64, lens, max_pages=3000), 2, 1, FP16, causal=True)
+    attend(make(1, 64, lens), 2, 9, FP16, causal=True)
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lens,T,rows", [
     ([300], 256, None), ([256], 256, None), ([1], 1, None), ([100, 3, 0], 3, [3, 3, 2]), ([500, 129, 64], 130, [130, 65, 1]),

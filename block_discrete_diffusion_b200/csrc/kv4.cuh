@@ -66,32 +66,44 @@ __device__ __forceinline__ float ue5m3_to_f32(uint32_t byte) {
 constexpr float kMaxScale = 10240.f;
 
 // Scale byte of a block whose largest magnitude is amax (NaN if one of its values is): amax / 6 to the
-// nearest ue5m3, ties to even.  amax has at most 11 significant bits, so the correctly rounded quotient lies
-// on a rounding border only when the exact one does.
+// nearest ue5m3, ties to even.  amax has at most 11 significant bits, so amax / 6 is either on a rounding border (at most
+// 5 bits) or off it by 2^-12 of itself: a product with 1 / 6, rounded to 16 bits, decides as the exact quotient does.
 __device__ __forceinline__ uint32_t ue5m3_scale(float amax) {
-  if (amax != amax) return 255u;
-  const float a = fminf(__fdiv_rn(amax, 6.f), kMaxScale);
-  if (a < 6.103515625e-05f) return (uint32_t)rintf(a * 131072.f);   // below 2^-14: steps of 2^-17
-  uint32_t u = __float_as_uint(a);
-  u += 0x7ffffu + ((u >> 20) & 1u);
-  return (u >> 20) - ((127u - 15u) << 3);
+  const float q = fminf(amax * 0.16666667f, kMaxScale);
+  uint32_t u = (__float_as_uint(q) + 0x80u) & ~0xffu;
+  // below 2^-14 steps of 2^-17: the sum's last bit is that step
+  const uint32_t small = __float_as_uint(__fadd_rn(__uint_as_float(u), 64.f)) & 15u;
+  u = ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
+  u = q < 6.103515625e-05f ? small : u;
+  return amax != amax ? 255u : u;
 }
 
-// Quotient x / s on the grid of 2^-16, from r = 1 / s.  The product errs by less than 2^-20 and an exact
+// Quotient x / s on the grid of 2^-16, from r = 1 / s to 2^-22.  The product errs by less than 2^-18 and an exact
 // quotient of an 11-bit value by a 4-bit scale is either on a border between two codes (a multiple of 1/4) or at
 // least 2^-13 away from it: on the grid every border case is met exactly, and ties go to the even code.
 __device__ __forceinline__ float on_grid(float x, float r) { return __fadd_rn(__fmaf_rn(x, r, 192.f), -192.f); }
 
-// two quotients as an e2m1 pair (lo in the low nibble), nearest, ties to even, beyond 6 saturating
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\t.reg .b16 h;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "mov.b16 h, {b, 0};\n\t"
-      "cvt.u32.u16 %0, h;\n\t}\n"
-      : "=r"(d)
-      : "f"(lo), "f"(hi));
-  return d;
+// four pairs of quotients as the e2m1 bytes of a word (first of a pair in the low nibble), nearest, ties to even,
+// beyond 6 saturating
+__device__ __forceinline__ uint32_t to_e2m1_word(float a0, float a1, float b0, float b1, float c0, float c1, float d0,
+                                                 float d1) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
+      : "=r"(w)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1), "f"(d0), "f"(d1));
+  return w;
+}
+
+// 1 / s, to 2^-23 (s a positive scale)
+__device__ __forceinline__ float fast_rcp(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {

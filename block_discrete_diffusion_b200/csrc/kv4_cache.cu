@@ -1,9 +1,10 @@
 // kv4_cache.cu -- the paged 4-bit cache: rows in and out, and its pages.
 //
 // Rows.  A CTA owns one (sequence, page, KV head) block, so every byte of a page has one writer.  A thread takes
-// whole words of the block (positions g and g + 8 of K, a quad of positions of V) with all 16 channels of a
-// scale: it needs no exchange with its neighbours, and only words that some other row shares are read first.
-// Bound by memory: a value costs 2 bytes on one side and 0.5625 on the other.
+// whole words of the block (positions g and g + 8 of K, a quad of positions of V) with 8 channels, so that a
+// row's loads and stores are contiguous over the lanes; two neighbours share a scale.  Only words that some other row
+// shares are read first.  Bound by memory: a value costs 2 bytes on one side and 0.5625 on the other; all of a
+// thread's loads are under way before the first is used (32 KB of rows a CTA).
 //
 // Pages.  The book (lengths, reference counts, tables) is a few hundred KB at most and its updates depend on one
 // another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left
@@ -23,59 +24,65 @@ bool first_on_device(unsigned long long* done) {
 
 namespace {
 
-// 16 elements (32 bytes) of a row
+// 8 elements (16 bytes) of a row
 template <typename T>
-__device__ __forceinline__ void load16(const void* base, long long at, float (&x)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+__device__ __forceinline__ uint4 load8(const void* base, long long at) {
+  return *reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at);
+}
+template <typename T>
+__device__ __forceinline__ void widen8(uint4 q, float (&x)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 q = p[i];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      x[8 * i + 2 * c] = Half<T>::lo(w[c]);
-      x[8 * i + 2 * c + 1] = Half<T>::hi(w[c]);
-    }
+  for (int c = 0; c < 4; ++c) {
+    x[2 * c] = Half<T>::lo(w[c]);
+    x[2 * c + 1] = Half<T>::hi(w[c]);
   }
 }
 template <typename T>
-__device__ __forceinline__ void store16(void* base, long long at, const float (&x)[16]) {
-  uint4* p = reinterpret_cast<uint4*>(static_cast<T*>(base) + at);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    p[i] = make_uint4(Half<T>::pack(x[8 * i], x[8 * i + 1]), Half<T>::pack(x[8 * i + 2], x[8 * i + 3]),
-                      Half<T>::pack(x[8 * i + 4], x[8 * i + 5]), Half<T>::pack(x[8 * i + 6], x[8 * i + 7]));
+__device__ __forceinline__ void store8(void* base, long long at, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(static_cast<T*>(base) + at) =
+      make_uint4(Half<T>::pack(x[0], x[1]), Half<T>::pack(x[2], x[3]), Half<T>::pack(x[4], x[5]),
+                 Half<T>::pack(x[6], x[7]));
 }
 
-// Scale byte of 16 values; the values become quotients on the grid that to_e2m1x2 rounds.
-__device__ __forceinline__ uint32_t to_quotients(float (&x)[16]) {
+// Scale byte of the 16 values that this lane and its neighbour (lane ^ 1) hold; the values become quotients on the grid
+// that to_e2m1_word rounds.  Both lanes take part.
+__device__ __forceinline__ uint32_t to_quotients(float (&x)[8]) {
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_nan(amax, fabsf(x[i]));
+  for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(x[i]));
+  amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const uint32_t byte = ue5m3_scale(amax);
   const float s = ue5m3_to_f32(byte);
-  const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+  const float r = s > 0.f ? fast_rcp(s) : 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = on_grid(x[i], r);
+  for (int i = 0; i < 8; ++i) x[i] = on_grid(x[i], r);
   return byte;
 }
 
-__device__ __forceinline__ void merge_words(uint4* p, uint4 v, uint32_t mask) {
-  if (mask == 0xffffffffu) {
-    *p = v;
-    return;
+// v's bits of `mask` into *p
+__device__ __forceinline__ void merge_words(uint2* p, uint2 v, uint32_t mask) {
+  if (mask != 0xffffffffu) {
+    const uint2 o = *p;
+    v = make_uint2((o.x & ~mask) | (v.x & mask), (o.y & ~mask) | (v.y & mask));
   }
-  const uint4 o = *p;
-  *p = make_uint4((o.x & ~mask) | (v.x & mask), (o.y & ~mask) | (v.y & mask), (o.z & ~mask) | (v.z & mask),
-                  (o.w & ~mask) | (v.w & mask));
+  *p = v;
+}
+__device__ __forceinline__ void merge_words(uint4* p, uint4 v, uint32_t mask) {
+  if (mask != 0xffffffffu) {
+    const uint4 o = *p;
+    v = make_uint4((o.x & ~mask) | (v.x & mask), (o.y & ~mask) | (v.y & mask), (o.z & ~mask) | (v.z & mask),
+                   (o.w & ~mask) | (v.w & mask));
+  }
+  *p = v;
 }
 
-constexpr int kRowThreads = 128;
-
-// Rows [len - n, len) of every sequence into (Write) or out of its pages.
+// Rows [len - n, len) of every sequence into (Write) or out of its pages.  2 DH threads: each takes two half blocks of
+// K (8 channels of two positions) and one of V (8 channels of four positions).
 template <int DH, typename T, bool Write>
-__global__ void __launch_bounds__(kRowThreads) kv4_rows_kernel(Kv4View c, int layer, Kv4Rows r) {
+__global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, Kv4Rows r) {
   using F = Kv4<DH>;
+  constexpr int kThreads = 2 * DH, kBlocks = DH / 16;
   pdl_trigger();
   pdl_wait();
   const int seq = blockIdx.z, head = blockIdx.y;
@@ -91,129 +98,146 @@ __global__ void __launch_bounds__(kRowThreads) kv4_rows_kernel(Kv4View c, int la
   const int lp = start / kPage + blockIdx.x;
   if ((long long)lp * kPage >= len) return;
   const int page = c.table[(size_t)seq * c.max_pages + lp];
-  if (page < 0 || page >= c.n_pages || (Write && c.refs[page] != 1)) {   // a shared page is nobody's to write
+  if (page < 0 || page >= c.n_pages) {
     if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
     return;
   }
+  const int owners = Write ? c.refs[page] : 1;   // (looked at before the first store)
   uint8_t* block = c.pool + (((size_t)layer * c.n_pages + page) * c.n_kv + head) * F::kBytes;
   const int lo = max(start - lp * kPage, 0), hi = min(len - lp * kPage, kPage);   // positions of this page
   const long long row0 = (long long)lp * kPage - start;                          // row of the page's position 0
   const long long kb = seq * r.k_seq + head * r.k_head, vb = seq * r.v_seq + head * r.v_head;
+  const int u = threadIdx.x & 1, b = threadIdx.x / 2 % kBlocks, rest = threadIdx.x / 2 / kBlocks;   // rest: 0 .. 15
 
-  // K: positions p and p + 8 of a tile, one block of 16 channels
-  for (int i = threadIdx.x; i < (kPage / 2) * (DH / 16); i += kRowThreads) {
-    const int b = i % (DH / 16), pair = i / (DH / 16);
-    const int kt = pair / 8, g = pair % 8, t = b / F::kH, jh = b % F::kH;
-    const int p0 = kt * 16 + g, p1 = p0 + 8;
-    const bool in0 = p0 >= lo && p0 < hi, in1 = p1 >= lo && p1 < hi;
-    if (!in0 && !in1) continue;
-    uint4* words = reinterpret_cast<uint4*>(block + ((kt * F::kH + jh) * 32 + g * 4 + t) * 16);
-    uint8_t* sc = block + F::kSk + (g * 4 + t) * 8 * F::kH + 2 * kt * F::kH + jh;   // position g; g + 8 is kH further
-    float x0[16], x1[16];
-    if (Write) {
+  // K: two pairs of positions p, p + 8
+  const int t = b / F::kH, jh = b % F::kH;
+  int kp[2];
+  bool in0[2], in1[2];
+  uint2* k_words[2];
+  uint8_t* k_scale[2];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x0[e] = x1[e] = 0.f;
-      if (in0) load16<T>(r.k, kb + (row0 + p0) * r.k_row + b * 16, x0);
-      if (in1) load16<T>(r.k, kb + (row0 + p1) * r.k_row + b * 16, x1);
+  for (int i = 0; i < 2; ++i) {
+    const int pair = rest + 16 * i, kt = pair / 8, g = pair % 8;
+    kp[i] = kt * 16 + g;
+    in0[i] = kp[i] >= lo && kp[i] < hi;
+    in1[i] = kp[i] + 8 >= lo && kp[i] + 8 < hi;
+    k_words[i] = reinterpret_cast<uint2*>(block + ((kt * F::kH + jh) * 32 + g * 4 + t) * 16) + u;
+    k_scale[i] = block + F::kSk + (g * 4 + t) * 8 * F::kH + 2 * kt * F::kH + jh;   // position p; p + 8 is kH further
+  }
+  // V: positions 2t, 2t + 1, 2t + 8, 2t + 9 of a tile
+  const int vt = rest / 4, vq = rest % 4, vp = vt * 16 + 2 * vq;
+  bool in[4];
+  uint32_t v_mask = 0, s_mask = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int p = vp + (e & 1) + 8 * (e >> 1);
+    in[e] = p >= lo && p < hi;
+    v_mask |= in[e] ? 0x0f0fu << (16 * (e >> 1) + 4 * (e & 1)) : 0u;
+    s_mask |= in[e] ? 0xffu << (8 * e) : 0u;
+  }
+  const int v_h = F::kH == 2 ? u : 0, v_g = F::kH == 2 ? b : 2 * b + u;
+  uint4* v_words = reinterpret_cast<uint4*>(block + F::kV + ((vt * F::kH + v_h) * 32 + v_g * 4 + vq) * 16);
+  uint32_t* v_scale = reinterpret_cast<uint32_t*>(block + F::kSv + ((b * 4 + vq) * 4 + vt) * 4);
+  const int ch = b * 16 + 8 * u;
+  auto k_at = [&](int p) { return kb + (row0 + p) * r.k_row + ch; };
+  auto v_at = [&](int e) { return vb + (row0 + vp + (e & 1) + 8 * (e >> 1)) * r.v_row + ch; };
+
+  if constexpr (Write) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 k0[2], k1[2], v[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k0[i] = in0[i] ? load8<T>(r.k, k_at(kp[i])) : zero;
+      k1[i] = in1[i] ? load8<T>(r.k, k_at(kp[i] + 8)) : zero;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = in[e] ? load8<T>(r.v, v_at(e)) : zero;
+    if (owners != 1) {   // a page with other owners is nobody's to write
+      if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!__any_sync(0xffffffffu, in0[i] || in1[i])) continue;   // (single tokens: most warps have nothing)
+      float x0[8], x1[8];
+      widen8<T>(k0[i], x0);
+      widen8<T>(k1[i], x1);
       const uint32_t s0 = to_quotients(x0), s1 = to_quotients(x1);
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = to_e2m1_word(x0[4 * j], x0[4 * j + 1], x1[4 * j], x1[4 * j + 1], x0[4 * j + 2], x0[4 * j + 3],
+                            x1[4 * j + 2], x1[4 * j + 3]);
+      if (in0[i] || in1[i])
+        merge_words(k_words[i], make_uint2(w[0], w[1]), (in0[i] ? 0x00ff00ffu : 0u) | (in1[i] ? 0xff00ff00u : 0u));
+      if (u == 0 && in0[i]) k_scale[i][0] = (uint8_t)s0;
+      if (u == 0 && in1[i]) k_scale[i][F::kH] = (uint8_t)s1;
+    }
+    if (!__any_sync(0xffffffffu, v_mask != 0)) return;
+    float x[4][8];
+    uint32_t s = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      widen8<T>(v[e], x[e]);
+      s |= to_quotients(x[e]) << (8 * e);
+    }
+    if (v_mask) {
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[j] = to_e2m1x2(x0[4 * j], x0[4 * j + 1]) | to_e2m1x2(x1[4 * j], x1[4 * j + 1]) << 8 |
-               to_e2m1x2(x0[4 * j + 2], x0[4 * j + 3]) << 16 | to_e2m1x2(x1[4 * j + 2], x1[4 * j + 3]) << 24;
-      merge_words(words, make_uint4(w[0], w[1], w[2], w[3]),
-                  (in0 ? 0x00ff00ffu : 0u) | (in1 ? 0xff00ff00u : 0u));
-      if (in0) sc[0] = (uint8_t)s0;
-      if (in1) sc[F::kH] = (uint8_t)s1;
-    } else {
-      const uint4 q = *words;
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      const float s0 = ue5m3_to_f32(sc[0]), s1 = ue5m3_to_f32(sc[F::kH]);
+        w[j] = to_e2m1_word(x[0][2 * j], x[1][2 * j], x[0][2 * j + 1], x[1][2 * j + 1], x[2][2 * j], x[3][2 * j],
+                            x[2][2 * j + 1], x[3][2 * j + 1]);
+      merge_words(v_words, make_uint4(w[0], w[1], w[2], w[3]), v_mask);
+      if (u == 0) *v_scale = s_mask == 0xffffffffu ? s : (*v_scale & ~s_mask) | (s & s_mask);
+    }
+  } else {
+    if (!__any_sync(0xffffffffu, in0[0] || in1[0] || in0[1] || in1[1] || v_mask)) return;
+    uint2 kw[2];
+    float ks0[2], ks1[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+    for (int i = 0; i < 2; ++i) {
+      kw[i] = *k_words[i];
+      ks0[i] = ue5m3_to_f32(k_scale[i][0]);
+      ks1[i] = ue5m3_to_f32(k_scale[i][F::kH]);
+    }
+    const uint4 vw = *v_words;
+    const uint32_t vs = *v_scale;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w[2] = {kw[i].x, kw[i].y};
+      float x0[8], x1[8];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
         uint32_t o[4];
         e2m1_to_f16(w[j], o);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x0[4 * j + 2 * e] = Half<__half>::lo(o[2 * e]) * s0;
-          x0[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e]) * s0;
-          x1[4 * j + 2 * e] = Half<__half>::lo(o[2 * e + 1]) * s1;
-          x1[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e + 1]) * s1;
+          x0[4 * j + 2 * e] = Half<__half>::lo(o[2 * e]) * ks0[i];
+          x0[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e]) * ks0[i];
+          x1[4 * j + 2 * e] = Half<__half>::lo(o[2 * e + 1]) * ks1[i];
+          x1[4 * j + 2 * e + 1] = Half<__half>::hi(o[2 * e + 1]) * ks1[i];
         }
       }
-      if (in0) store16<T>(r.k, kb + (row0 + p0) * r.k_row + b * 16, x0);
-      if (in1) store16<T>(r.k, kb + (row0 + p1) * r.k_row + b * 16, x1);
+      if (in0[i]) store8<T>(r.k, k_at(kp[i]), x0);
+      if (in1[i]) store8<T>(r.k, k_at(kp[i] + 8), x1);
     }
-  }
-
-  // V: positions 2t, 2t + 1, 2t + 8, 2t + 9 of a tile, one block of 16 channels
-  for (int i = threadIdx.x; i < 16 * (DH / 16); i += kRowThreads) {
-    const int b = i % (DH / 16), quad = i / (DH / 16);
-    const int kt = quad / 4, t = quad % 4;
-    const int p0 = kt * 16 + 2 * t;
-    bool in[4];
-    uint32_t mask = 0;
+    const uint32_t w[4] = {vw.x, vw.y, vw.z, vw.w};
+    float x[4][8], sv[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p = p0 + (e & 1) + 8 * (e >> 1);
-      in[e] = p >= lo && p < hi;
-      mask |= in[e] ? 0x0f0fu << (16 * (e >> 1) + 4 * (e & 1)) : 0u;
-    }
-    if (!mask) continue;
-    // channels 8 u .. 8 u + 7 of the block: the words of one (h, lane)
-    uint4* words[2];
+    for (int e = 0; e < 4; ++e) sv[e] = ue5m3_to_f32((vs >> (8 * e)) & 0xff);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int jh = F::kH == 2 ? u : 0, g = F::kH == 2 ? b : 2 * b + u;
-      words[u] = reinterpret_cast<uint4*>(block + F::kV + ((kt * F::kH + jh) * 32 + g * 4 + t) * 16);
-    }
-    uint32_t* sc = reinterpret_cast<uint32_t*>(block + F::kSv + ((b * 4 + t) * 4 + kt) * 4);
-    float x[4][16];
-    if (Write) {
-      uint32_t s = 0, smask = 0;
+    for (int j = 0; j < 4; ++j) {
+      uint32_t o[4];
+      e2m1_to_f16(w[j], o);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[e][k] = 0.f;
-        if (in[e]) load16<T>(r.v, vb + (row0 + p0 + (e & 1) + 8 * (e >> 1)) * r.v_row + b * 16, x[e]);
-        s |= to_quotients(x[e]) << (8 * e);
-        smask |= in[e] ? 0xffu << (8 * e) : 0u;
+      for (int e = 0; e < 4; ++e) {   // o[e]: channel e & 1, positions 2 (e >> 1) + {0, 1} of the quad
+        x[2 * (e >> 1)][2 * j + (e & 1)] = Half<__half>::lo(o[e]) * sv[2 * (e >> 1)];
+        x[2 * (e >> 1) + 1][2 * j + (e & 1)] = Half<__half>::hi(o[e]) * sv[2 * (e >> 1) + 1];
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = 8 * u + 2 * j;
-          w[j] = to_e2m1x2(x[0][k], x[1][k]) | to_e2m1x2(x[0][k + 1], x[1][k + 1]) << 8 |
-                 to_e2m1x2(x[2][k], x[3][k]) << 16 | to_e2m1x2(x[2][k + 1], x[3][k + 1]) << 24;
-        }
-        merge_words(words[u], make_uint4(w[0], w[1], w[2], w[3]), mask);
-      }
-      *sc = smask == 0xffffffffu ? s : (*sc & ~smask) | (s & smask);
-    } else {
-      float s[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = ue5m3_to_f32((*sc >> (8 * e)) & 0xff);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 q = *words[u];
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t o[4];
-          e2m1_to_f16(w[j], o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {   // o[e]: channel e & 1, positions 2 (e >> 1) + {0, 1} of the quad
-            x[2 * (e >> 1)][8 * u + 2 * j + (e & 1)] = Half<__half>::lo(o[e]) * s[2 * (e >> 1)];
-            x[2 * (e >> 1) + 1][8 * u + 2 * j + (e & 1)] = Half<__half>::hi(o[e]) * s[2 * (e >> 1) + 1];
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (in[e]) store16<T>(r.v, vb + (row0 + p0 + (e & 1) + 8 * (e >> 1)) * r.v_row + b * 16, x[e]);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (in[e]) store8<T>(r.v, v_at(e), x[e]);
   }
 }
 
@@ -221,8 +245,8 @@ template <int DH, typename T>
 cudaError_t launch_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st) {
   const int pages = (int)(((long long)r.rows + kPage - 2) / kPage + 1);   // the rows may begin at a page's last position
   const dim3 grid(pages < c.max_pages ? pages : c.max_pages, c.n_kv, c.n_seq);
-  return launch_k(write ? kv4_rows_kernel<DH, T, true> : kv4_rows_kernel<DH, T, false>, grid, dim3(kRowThreads), 0, st,
-                  1, c, layer, r);
+  return launch_k(write ? kv4_rows_kernel<DH, T, true> : kv4_rows_kernel<DH, T, false>, grid, dim3(2 * DH), 0, st, 1, c,
+                  layer, r);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -8,7 +8,8 @@
 //
 // Pages.  The book (lengths, reference counts, tables) is a few hundred KB at most and its updates depend on one
 // another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left
-// as a list of (from, to) for a second launch over the whole GPU.  Nothing changes when a call cannot be
+// as a list of (from, to) for a second launch over the whole GPU (whose CTAs are placed while the first runs; one launch
+// whose other CTAs wait for the list measured 33.5 us instead of 23.5 for 32 copies of 2.2 MB).  Nothing changes when a call cannot be
 // carried out whole: the error word tells.
 #include "kv4.cuh"
 #include "kv4_kernels.h"
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kBookThreads) kv4_extend_kernel(Kv4View c, con
       k += v[e];
     }
     int found;
-    int rank = n_free + block_scan(k, &found);
+    const int before = n_free;   // (read before the scan's barriers: thread 0 adds to it after them)
+    int rank = before + block_scan(k, &found);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (v[e]) {
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kBookThreads) kv4_compact_kernel(Kv4View c) {
 // Page contents: move m takes page move_src[m] to move_dst[m] in every layer.  No page is both a source and a
 // destination, so the order does not matter.  With Remap the page tables follow (c.map of a moved page).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveChunk = kMoveThreads * 16 * 4;   // bytes a CTA copies at a time: 4 loads in flight a thread
+constexpr int kMoveChunk = kMoveThreads * 16 * 8;   // bytes a CTA copies at a time: 8 loads in flight a thread
 
 template <bool Remap>
 __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4View c, size_t page_bytes) {
@@ -531,12 +533,12 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4View c, size_
     const uint4* s = reinterpret_cast<const uint4*>(c.pool + (plane + c.move_src[m]) * page_bytes + off);
     uint4* d = reinterpret_cast<uint4*>(c.pool + (plane + c.move_dst[m]) * page_bytes + off);
     const int n = (int)(min((size_t)kMoveChunk, page_bytes - off) / 16);
-    uint4 v[4];
+    uint4 v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 8; ++e)
       if (e * kMoveThreads + (int)threadIdx.x < n) v[e] = s[e * kMoveThreads + threadIdx.x];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < 8; ++e)
       if (e * kMoveThreads + (int)threadIdx.x < n) d[e * kMoveThreads + threadIdx.x] = v[e];
   }
   if (Remap && moves > 0) {
@@ -550,10 +552,14 @@ __global__ void __launch_bounds__(kMoveThreads) kv4_move_kernel(Kv4View c, size_
   }
 }
 
+// For at most `moves` moved pages.  Sixteen CTAs an SM where there can be that much work: with the eight that fit at
+// once half of a 30-layer pool took 93 us instead of 85.
 template <bool Remap>
-cudaError_t launch_moves(const Kv4View& c, int n_sms, cudaStream_t st) {
+cudaError_t launch_moves(const Kv4View& c, long long moves, int n_sms, cudaStream_t st) {
   const size_t page_bytes = (size_t)c.n_kv * 72 * c.dh;
-  return launch_k(kv4_move_kernel<Remap>, dim3(8 * n_sms), dim3(kMoveThreads), 0, st, 1, c, page_bytes);
+  const long long work = moves * c.n_layers * (long long)((page_bytes + kMoveChunk - 1) / kMoveChunk);
+  const int grid = (int)(work < 16 * n_sms ? work + 1 : 16 * n_sms);
+  return launch_k(kv4_move_kernel<Remap>, dim3(grid), dim3(kMoveThreads), 0, st, 1, c, page_bytes);
 }
 
 }  // namespace
@@ -568,7 +574,7 @@ cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, 
 
 cudaError_t kv4_extend(const Kv4View& c, const int32_t* counts, int n_sms, cudaStream_t st) {
   const cudaError_t e = launch_k(kv4_extend_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c, counts);
-  return e != cudaSuccess ? e : launch_moves<false>(c, n_sms, st);
+  return e != cudaSuccess ? e : launch_moves<false>(c, c.n_seq, n_sms, st);   // a copy for each sequence at most
 }
 
 cudaError_t kv4_fork(const Kv4View& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st) {
@@ -581,7 +587,7 @@ cudaError_t kv4_free(const Kv4View& c, const int32_t* slots, int n, cudaStream_t
 
 cudaError_t kv4_compact(const Kv4View& c, int n_sms, cudaStream_t st) {
   const cudaError_t e = launch_k(kv4_compact_kernel, dim3(1), dim3(kBookThreads), 0, st, 1, c);
-  return e != cudaSuccess ? e : launch_moves<true>(c, n_sms, st);
+  return e != cudaSuccess ? e : launch_moves<true>(c, c.n_pages / 2, n_sms, st);   // as many holes as moves
 }
 
 }  // namespace dg

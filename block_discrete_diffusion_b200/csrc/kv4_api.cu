@@ -98,23 +98,27 @@ struct Plan {
   static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
 };
 
-// Rows of a KV head up to which the few-rows form runs.
-constexpr int kFewRows = 16;
+// Rows of a KV head up to which the few-rows form runs whatever the lengths (32 sequences of 8192 positions, 8 KV heads:
+// 8 rows 68 us, 32 rows 208 us, 64 rows 402 us; the other form 258 to 262 us for any of them).
+constexpr int kFewRows = 32;
 
 Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
   Plan p{};
-  p.few = (long long)rows * (n_q / c->n_kv) <= kFewRows;
   const int sms = current_sms();
+  const long long group_rows = (long long)rows * (n_q / c->n_kv);
+  const int few_ctas = sms * (c->d_head == 128 ? 3 : 5);   // what fits the SMs' shared memory at once
+  // A cluster for each unit where the sequences cannot be long: one launch and no parts in memory (one token behind
+  // 577 positions: 11.7 -> 7.0 us; 64 rows behind 1024: 9.7 us, 21.8 in the many-rows form).  Longer units want more warps
+  // than a cluster of such CTAs has (32768 positions: 21.2 us on the line, 24.8 in clusters of 16 CTAs, 24.3 of 12-warp
+  // CTAs that fill an SM), and units of different lengths leave SMs idle: from about 24 pages a CTA on that costs
+  // more than the second launch.
+  const long long units = (group_rows + kKv4FewTile - 1) / kKv4FewTile * c->n_kv * c->n_seq;
+  int n = kKv4MaxCluster;
+  while (n > 1 && units * n > few_ctas) n /= 2;
+  if (units <= few_ctas && c->max_pages <= 24 * n) p.cluster = n;
+  p.few = p.cluster || group_rows <= kFewRows;
   if (p.few) {
-    p.n_ctas = sms * (c->d_head == 128 ? 3 : 5);   // what fits the SMs' shared memory at once
-    // A cluster for each unit where the sequences cannot be long: one launch and no parts in memory (one token behind
-    // 577 positions: 11.7 -> 7.0 us).  Longer units want more warps than a cluster of such CTAs has (32768 positions:
-    // 21.2 us on the line, 24.8 in clusters of 16 CTAs, 24.3 of 12-warp CTAs that fill an SM), and units of different lengths
-    // leave SMs idle: from about 24 pages a CTA on that costs more than the second launch.
-    const long long units = ((long long)rows * (n_q / c->n_kv) + kKv4FewTile - 1) / kKv4FewTile * c->n_kv * c->n_seq;
-    int n = kKv4MaxCluster;
-    while (n > 1 && units * n > p.n_ctas) n /= 2;
-    if (units <= p.n_ctas && c->max_pages <= 24 * n) p.cluster = n;
+    p.n_ctas = few_ctas;
     p.min_share = 4;                               // a page for each warp
     p.tile = kKv4FewTile;
     p.row_bytes = 4 * (size_t)c->d_head;

@@ -110,6 +110,9 @@ def attend(c, n_q, T, dtype, rows=None, causal=False, seed=1, layer=0, scale=Non
     return q, out, lse
 
 
+# pages of a sequence's table: as many as it has, or as many as a long context has. It decides how the work is divided and
+# with few rows or short tables which form of the attention runs, and nothing else
+TABLES = [None, 3000]
 LENS = [[1], [0, 5, 64], [63, 64, 65], [127, 128, 129, 200], [700, 1, 257, 0, 513]]
 
 
@@ -140,8 +143,16 @@ def test_many_short_sequences(n_seq):
     ([300], 256, None), ([256], 256, None), ([1], 1, None), ([100, 3, 0], 3, [3, 3, 2]), ([500, 129, 64], 130, [130, 65, 1]),
     ([5, 700], 40, [40, 0]), ([64, 128, 192, 320], 64, None), ([1000], 17, None), ([2], 256, None)], ids=str)
 @pytest.mark.parametrize("n_q,n_kv,dh,dtype", [(16, 8, 128, BF16), (4, 2, 64, FP16), (3, 1, 128, FP16), (2, 2, 64, BF16)])
-def test_rows(lens, T, rows, causal, n_q, n_kv, dh, dtype):
-    attend(make(n_kv, dh, lens), n_q, T, dtype, rows=rows, causal=causal)
+@pytest.mark.parametrize("table", TABLES)
+def test_rows(lens, T, rows, causal, n_q, n_kv, dh, dtype, table):
+    attend(make(n_kv, dh, lens, max_pages=table), n_q, T, dtype, rows=rows, causal=causal)
+
+
+def test_many_query_heads():
+    """More rows of a KV head than a tile has, from one position."""
+    attend(make(1, 64, [100, 333], max_pages=3000), 40, 1, BF16)
+    attend(make(1, 128, [100, 333]), 300, 1, FP16)
+    attend(make(2, 128, [100, 333], max_pages=3000), 300, 3, FP16, causal=True)
 
 
 @pytest.mark.parametrize("T", [1, 9, 200])
@@ -150,15 +161,15 @@ def test_long_ragged_lengths(T):
 
 
 @pytest.mark.parametrize("q_scale,dtype", [(1e-30, BF16), (1e30, BF16), (1e-5, FP16), (500.0, FP16), (0.0, BF16)])
-@pytest.mark.parametrize("T", [1, 130])
-def test_magnitudes_of_q(q_scale, dtype, T):
-    c = make(1, 128, [200, 3])
+@pytest.mark.parametrize("T,table", [(1, None), (1, 3000), (130, 3000)])
+def test_magnitudes_of_q(q_scale, dtype, T, table):
+    c = make(1, 128, [200, 3], max_pages=table)
     attend(c, 2, T, dtype, q_scale=q_scale, scale=0.05 / max(q_scale, 1e-3) if q_scale else None)
 
 
-@pytest.mark.parametrize("T", [1, 33])
-def test_strides(T):
-    c = make(2, 64, [130, 77])
+@pytest.mark.parametrize("T,table", [(1, None), (33, None), (33, 3000)])
+def test_strides(T, table):
+    c = make(2, 64, [130, 77], max_pages=table)
     g = torch.Generator(device="cuda").manual_seed(3)
     qkv = torch.randn((2, T, 4 + 2 + 2, 64), generator=g, device="cuda").to(BF16)       # heads of a packed projection
     q = qkv[:, :, :4]
@@ -174,11 +185,11 @@ def test_strides(T):
 def test_pages_beyond_4_gib():
     layers, n_kv, dh = 1, 8, 128
     n_pages = 66000                                                                     # 4.9 GB
-    c = dg.dg_kv4_cache(layers, n_kv, dh, n_pages, 1, 3)
-    small = make(n_kv, dh, [150], spare=0)
+    c = dg.dg_kv4_cache(layers, n_kv, dh, n_pages, 1, 3000)
+    small = make(n_kv, dh, [150], spare=0, max_pages=3000)
     top = [n_pages - 1, n_pages - 3, n_pages - 2]
-    c.pool.view(n_pages, -1)[dev(top, torch.int64)] = small.pool.view(3, -1)[small.table[0].long()]
-    c.table[0] = dev(top)
+    c.pool.view(n_pages, -1)[dev(top, torch.int64)] = small.pool.view(3, -1)[small.table[0, :3].long()]
+    c.table[0, :3] = dev(top)
     c.lens[0] = 150
     for T in (1, 140):
         q = torch.randn((1, T, 16, dh), device="cuda").to(BF16)
@@ -191,10 +202,10 @@ def test_pages_beyond_4_gib():
         assert torch.equal(*outs)
 
 
-@pytest.mark.parametrize("T", [1, 40])
-def test_non_finite_values(T):
+@pytest.mark.parametrize("T,table", [(1, None), (40, None), (40, 3000)])
+def test_non_finite_values(T, table):
     """A NaN among the cached values reaches the rows that see it; a row of q that is not finite makes its own row NaN only."""
-    c = make(2, 64, [100, 100])
+    c = make(2, 64, [100, 100], max_pages=table)
     x = torch.zeros((2, 1, 2, 64), device="cuda").to(BF16)
     x[1, 0, 1, 5] = float("nan")
     dg.dg_kv4_append(c, 0, x, x)

@@ -17,6 +17,7 @@
 
 #include "dg.h"
 #include "dg_kernels.h"
+#include "kv4_kernels.h"
 
 #define DG_API extern "C" __attribute__((visibility("default")))
 
@@ -1015,6 +1016,53 @@ DG_API dg_status dg_load_prefix(dg_seqs* s, int seq, int P, const void* const* h
     CK(load_prefix(static_cast<const __nv_bfloat16*>(h_k[l]), static_cast<const __nv_bfloat16*>(h_v[l]), P, c.n_kv,
                    c.d_head, s->max_ctx, kc, vt, s->st));
   }
+  CK(add_to_P(s->seqP, seq, 1, P - s->P[seq], s->st));
+  s->P[seq] = P;
+  return DG_OK;
+}
+
+namespace {
+
+// One sequence's committed prefix into or out of a 4-bit cache, layer by layer.
+dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_cache* cache, int slot, bool store) {
+  if (!s) return fail(DG_ERR_INVALID_ARG, "%s: seqs is null", fn);
+  const dg_status st = kv4_check_cache(fn, cache);
+  if (st != DG_OK) return st;
+  const dg_model_config& c = s->m->cfg;
+  if (seq < 0 || seq >= s->n_seq) return fail(DG_ERR_INVALID_ARG, "%s: seq %d out of range", fn, seq);
+  if (slot < 0 || slot >= cache->n_seq) return fail(DG_ERR_INVALID_ARG, "%s: slot %d out of range", fn, slot);
+  if (cache->n_layers != c.n_layers || cache->n_kv != c.n_kv || cache->d_head != c.d_head)
+    return fail(DG_ERR_INVALID_ARG, "%s: the cache's layers, KV heads or d_head are not the model's", fn);
+  if (P < 0 || P + kCanvas > s->max_ctx) return fail(DG_ERR_CAPACITY, "%s: prefix %d + canvas exceeds max_ctx", fn, P);
+  if (P > (long long)cache->max_pages * DG_KV4_PAGE)
+    return fail(DG_ERR_CAPACITY, "%s: prefix %d exceeds the cache's %d pages a sequence", fn, P, cache->max_pages);
+  const size_t per_seq = (size_t)c.n_kv * s->max_ctx * c.d_head;
+  for (int l = 0; l < c.n_layers && P > 0; ++l) {
+    Kv4Rows r{};
+    r.k = s->kc + (size_t)l * layer_kv_elems(s) + (size_t)seq * per_seq;
+    r.v = s->vt + (size_t)l * layer_kv_elems(s) + (size_t)seq * per_seq;
+    r.k_row = c.d_head;
+    r.v_row = s->max_ctx;
+    r.k_head = r.v_head = (long long)s->max_ctx * c.d_head;
+    r.rows = P;
+    r.only = slot + 1;
+    CK(kv4_rows(kv4_view(cache), l, r, store, s->st));
+  }
+  return DG_OK;
+}
+
+}  // namespace
+
+DG_API dg_status dg_store_prefix_kv4(dg_seqs* s, int seq, const dg_kv4_cache* cache, int slot) {
+  NvtxRange nvtx_range("dg_store_prefix_kv4");
+  const int P = s && seq >= 0 && seq < s->n_seq ? s->P[seq] : 0;
+  return move_prefix("dg_store_prefix_kv4", s, seq, P, cache, slot, true);
+}
+
+DG_API dg_status dg_load_prefix_kv4(dg_seqs* s, int seq, int P, const dg_kv4_cache* cache, int slot) {
+  NvtxRange nvtx_range("dg_load_prefix_kv4");
+  const dg_status st = move_prefix("dg_load_prefix_kv4", s, seq, P, cache, slot, false);
+  if (st != DG_OK) return st;
   CK(add_to_P(s->seqP, seq, 1, P - s->P[seq], s->st));
   s->P[seq] = P;
   return DG_OK;

@@ -145,10 +145,13 @@ dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_
 
 Kv4Rows rows_of(const dg_kv4_rows* r) {
   return Kv4Rows{r->k, r->v, r->k_seq, r->k_row, r->k_head, r->v_seq, r->v_row, r->v_head, r->d_rows, r->rows,
-                 r->dtype == DG_DTYPE_FP16};
+                 r->dtype == DG_DTYPE_FP16, 0};
 }
 
 }  // namespace
+
+dg_status dg::kv4_check_cache(const char* fn, const dg_kv4_cache* c) { return check_cache(fn, c); }
+Kv4View dg::kv4_view(const dg_kv4_cache* c) { return view(c); }
 
 DG_API size_t dg_kv4_pool_bytes(const dg_kv4_cache* c) { return shape_error(c) ? 0 : pool_bytes(c); }
 DG_API size_t dg_kv4_book_bytes(const dg_kv4_cache* c) { return shape_error(c) ? 0 : 4 * book_words(c); }

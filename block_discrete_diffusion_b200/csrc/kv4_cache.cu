@@ -11,6 +11,8 @@
 // as a list of (from, to) for a second launch over the whole GPU (whose CTAs are placed while the first runs; one launch
 // whose other CTAs wait for the list measured 33.5 us instead of 23.5 for 32 copies of 2.2 MB).  Nothing changes when a call cannot be
 // carried out whole: the error word tells.
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "kv4_kernels.h"
 
@@ -78,18 +80,35 @@ __device__ __forceinline__ void merge_words(uint4* p, uint4 v, uint32_t mask) {
   *p = v;
 }
 
+// 8 channels of two neighbouring positions of a transposed V (positions side by side, channels `stride` elements apart): each
+// word holds both positions of a channel
+template <typename T>
+__device__ __forceinline__ void load_pairs(const void* base, long long at, long long stride, float (&x0)[8],
+                                           float (&x1)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const T*>(base) + at + c * stride);
+    x0[c] = Half<T>::lo(w);
+    x1[c] = Half<T>::hi(w);
+  }
+}
+
 // Rows [len - n, len) of every sequence into (Write) or out of its pages.  2 DH threads: each takes two half blocks of
-// K (8 channels of two positions) and one of V (8 channels of four positions).
-template <int DH, typename T, bool Write>
+// K (8 channels of two positions) and one of V (8 channels of four positions).  Whole: one sequence's prefix, V transposed.
+template <int DH, typename T, bool Write, bool Whole>
 __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, Kv4Rows r) {
   using F = Kv4<DH>;
   constexpr int kThreads = 2 * DH, kBlocks = DH / 16;
   pdl_trigger();
   pdl_wait();
-  const int seq = blockIdx.z, head = blockIdx.y;
+  const int seq = Whole ? r.only - 1 : blockIdx.z, head = blockIdx.y;
   const int len = c.lens[seq];
   const int n = r.n_rows ? r.n_rows[seq] : r.rows;
-  if (n == 0) return;
+  if (n == 0 && !Whole) return;
+  if (Whole && n != len) {
+    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_COUNT);
+    return;
+  }
   const long long cap = (long long)c.max_pages * kPage;
   if (n < 0 || n > r.rows || n > len || len > cap) {
     if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_COUNT);
@@ -107,7 +126,8 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
   uint8_t* block = c.pool + (((size_t)layer * c.n_pages + page) * c.n_kv + head) * F::kBytes;
   const int lo = max(start - lp * kPage, 0), hi = min(len - lp * kPage, kPage);   // positions of this page
   const long long row0 = (long long)lp * kPage - start;                          // row of the page's position 0
-  const long long kb = seq * r.k_seq + head * r.k_head, vb = seq * r.v_seq + head * r.v_head;
+  const long long kb = (Whole ? 0 : seq * r.k_seq) + head * r.k_head;
+  const long long vb = (Whole ? 0 : seq * r.v_seq) + head * r.v_head;
   const int u = threadIdx.x & 1, b = threadIdx.x / 2 % kBlocks, rest = threadIdx.x / 2 / kBlocks;   // rest: 0 .. 15
 
   // K: two pairs of positions p, p + 8
@@ -141,6 +161,9 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
   uint32_t* v_scale = reinterpret_cast<uint32_t*>(block + F::kSv + ((b * 4 + vq) * 4 + vt) * 4);
   const int ch = b * 16 + 8 * u;
   auto k_at = [&](int p) { return kb + (row0 + p) * r.k_row + ch; };
+  // (Whole: channel ch of position p; a pair's two positions share a word, which lies inside the caller's rows of
+  // positions even where the second one is behind the end)
+  auto vt_at = [&](int pair) { return vb + ch * r.v_row + lp * (long long)kPage + vp + 8 * pair; };
   auto v_at = [&](int e) { return vb + (row0 + vp + (e & 1) + 8 * (e >> 1)) * r.v_row + ch; };
 
   if constexpr (Write) {
@@ -151,8 +174,18 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
       k0[i] = in0[i] ? load8<T>(r.k, k_at(kp[i])) : zero;
       k1[i] = in1[i] ? load8<T>(r.k, k_at(kp[i] + 8)) : zero;
     }
+    float x[4][8];
+    if constexpr (Whole) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = in[e] ? load8<T>(r.v, v_at(e)) : zero;
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[e][k] = 0.f;
+      if (in[0]) load_pairs<T>(r.v, vt_at(0), r.v_row, x[0], x[1]);
+      if (in[2]) load_pairs<T>(r.v, vt_at(1), r.v_row, x[2], x[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = in[e] ? load8<T>(r.v, v_at(e)) : zero;
+    }
     if (owners != 1) {   // a page with other owners is nobody's to write
       if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
       return;
@@ -175,11 +208,10 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
       if (u == 0 && in1[i]) k_scale[i][F::kH] = (uint8_t)s1;
     }
     if (!__any_sync(0xffffffffu, v_mask != 0)) return;
-    float x[4][8];
     uint32_t s = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      widen8<T>(v[e], x[e]);
+      if constexpr (!Whole) widen8<T>(v[e], x[e]);
       s |= to_quotients(x[e]) << (8 * e);
     }
     if (v_mask) {
@@ -236,18 +268,38 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
         x[2 * (e >> 1) + 1][2 * j + (e & 1)] = Half<__half>::hi(o[e]) * sv[2 * (e >> 1) + 1];
       }
     }
+    if constexpr (Whole) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (in[e]) store8<T>(r.v, v_at(e), x[e]);
+      for (int pair = 0; pair < 2; ++pair)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          T* dst = static_cast<T*>(r.v) + vt_at(pair) + k * r.v_row;
+          const uint32_t w = Half<T>::pack(x[2 * pair][k], x[2 * pair + 1][k]);
+          if (in[2 * pair + 1])
+            *reinterpret_cast<uint32_t*>(dst) = w;
+          else if (in[2 * pair])   // (the position behind the prefix stays as it was)
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)w;
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in[e]) store8<T>(r.v, v_at(e), x[e]);
+    }
   }
 }
 
 template <int DH, typename T>
 cudaError_t launch_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st) {
   const int pages = (int)(((long long)r.rows + kPage - 2) / kPage + 1);   // the rows may begin at a page's last position
-  const dim3 grid(pages < c.max_pages ? pages : c.max_pages, c.n_kv, c.n_seq);
-  return launch_k(write ? kv4_rows_kernel<DH, T, true> : kv4_rows_kernel<DH, T, false>, grid, dim3(2 * DH), 0, st, 1, c,
-                  layer, r);
+  const dim3 grid(pages < c.max_pages ? pages : c.max_pages, c.n_kv, r.only ? 1 : c.n_seq);
+  if (r.only) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return launch_k(write ? kv4_rows_kernel<DH, T, true, true> : kv4_rows_kernel<DH, T, false, true>, grid,
+                      dim3(2 * DH), 0, st, 1, c, layer, r);
+    return cudaErrorInvalidValue;
+  }
+  return launch_k(write ? kv4_rows_kernel<DH, T, true, false> : kv4_rows_kernel<DH, T, false, false>, grid, dim3(2 * DH),
+                  0, st, 1, c, layer, r);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -28,6 +28,9 @@ struct Kv4Rows {
   const int32_t* n_rows;   // rows of each sequence (null: `rows` each)
   int rows;
   int fp16;                // element type: bf16 (0) or fp16 (1)
+  // One sequence's whole prefix instead of all sequences' last rows: sequence only - 1 (0: all), whose length has to
+  // be `rows`; v then has its positions side by side and its channels v_row apart (bf16).
+  int only;
 };
 
 cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st);
@@ -61,6 +64,10 @@ constexpr int kKv4ManyTile = 256, kKv4ManyStep = 64;
 cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st);
+
+// the checks of a cache's shape and buffers that every entry point makes, and its device view
+dg_status kv4_check_cache(const char* fn, const dg_kv4_cache* c);
+Kv4View kv4_view(const dg_kv4_cache* c);
 
 // kernel attributes are per device: true the first time `done` (one per kernel) meets the current device
 bool first_on_device(unsigned long long* done);

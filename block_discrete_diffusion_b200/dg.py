@@ -28,6 +28,7 @@ ENTRY_POINTS = (
     "dg_block_commit_last_kv", "dg_head_sample_workspace_bytes", "dg_head_sample", "dg_head_sample_error",
     "dg_kv4_pool_bytes", "dg_kv4_book_bytes", "dg_kv4_init", "dg_kv4_extend", "dg_kv4_fork", "dg_kv4_free",
     "dg_kv4_compact", "dg_kv4_append", "dg_kv4_read", "dg_kv4_attend_workspace_bytes", "dg_kv4_attend", "dg_kv4_error",
+    "dg_store_prefix_kv4", "dg_load_prefix_kv4",
 )
 
 # dg_kernel_class, in order
@@ -155,6 +156,8 @@ def lib():
         L.dg_kv4_attend_workspace_bytes.restype = c_size_t
         L.dg_kv4_attend.argtypes = [C, c_int, P(dg_kv4_attn), c_void_p, c_size_t, c_void_p]
         L.dg_kv4_error.argtypes = [C, c_void_p, P(c_int)]
+        L.dg_store_prefix_kv4.argtypes = [c_void_p, c_int, C, c_int]
+        L.dg_load_prefix_kv4.argtypes = [c_void_p, c_int, c_int, C, c_int]
         L.dg_device_error.argtypes = [c_void_p, P(c_int)]
         L.dg_stats_reset.argtypes = [c_void_p, c_int]
         L.dg_stats_read.argtypes = [c_void_p, c_void_p, c_void_p]
@@ -510,6 +513,18 @@ def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale
                     shape[1], code, int(bool(causal)), c.d_head ** -0.5 if scale is None else scale)
     _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), _ptr(ws),
                                                 ws.numel() * ws.element_size(), _kv4_stream(cache, stream)))
+
+
+def dg_store_prefix_kv4(seqs: Seqs, seq, cache: Kv4Cache, slot):
+    """The committed prefix of sequence seq into the cache's sequence slot (grown to that length before)."""
+    _kv4_stream(cache, seqs.stream)
+    _check("dg_store_prefix_kv4", lib().dg_store_prefix_kv4(seqs.handle, seq, cache.ref, slot))
+
+
+def dg_load_prefix_kv4(seqs: Seqs, seq, P, cache: Kv4Cache, slot):
+    """The prefix of length P that the cache's sequence slot holds as sequence seq's."""
+    _kv4_stream(cache, seqs.stream)
+    _check("dg_load_prefix_kv4", lib().dg_load_prefix_kv4(seqs.handle, seq, P, cache.ref, slot))
 
 
 def dg_kv4_error(cache: Kv4Cache, stream=None) -> int:

@@ -364,6 +364,16 @@ size_t dg_kv4_attend_workspace_bytes(const dg_kv4_cache *c, int n_q, int rows);
 dg_status dg_kv4_attend(const dg_kv4_cache *c, int layer, const dg_kv4_attn *a, void *ws, size_t ws_bytes,
                         void *stream);
 
+/* A sequence set's prefix and such a cache: a sequence that waits (a turn of a conversation, a prompt that others will
+ * share) is held in 4 bits and its rows of the set are given to another.  dg_store_prefix_kv4 quantises the committed
+ * prefix [0, P) of sequence `seq`, every layer, into the cache's sequence `slot`, which has length P (dg_kv4_extend)
+ * and pages without other owners; dg_load_prefix_kv4 installs the prefix that `slot` holds, of length P, as sequence
+ * `seq`'s (replacing its cache content, as dg_load_prefix does).  The cache has the model's layers, KV heads and
+ * d_head.  Enqueued on the handle's stream; a length other than P is recorded in the cache's book (code 8) and moves
+ * nothing. */
+dg_status dg_store_prefix_kv4(dg_seqs *s, int seq, const dg_kv4_cache *cache, int slot);
+dg_status dg_load_prefix_kv4(dg_seqs *s, int seq, int P, const dg_kv4_cache *cache, int slot);
+
 /* Synchronise the stream and return the first device-side error code recorded in the book since the last call
  * (0 = none); the record is cleared.  Returns DG_ERR_DEVICE if non-zero. */
 dg_status dg_kv4_error(const dg_kv4_cache *c, void *stream, int *h_code);

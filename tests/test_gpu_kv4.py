@@ -525,3 +525,80 @@ def test_long_lengths_with_few_and_many_rows(causal):
     """Sequences whose rows fill one 128-row tile, two, or part of one, long enough for many steps of each."""
     attend(make(2, 128, [5000, 3001, 4097, 2500]), 4, 256, BF16, rows=[40, 256, 64, 65], causal=causal)
     attend(make(1, 64, [4000, 6000]), 1, 130, FP16, rows=[129, 128], causal=causal)
+
+
+# ---------------------------------------------------------------------------------------------
+# a sequence set's prefixes
+# ---------------------------------------------------------------------------------------------
+def kv_views(seqs):
+    """K [L, n_seq, n_kv, max_ctx, dh] and V transposed [L, n_seq, n_kv, dh, max_ctx] of a set's cache."""
+    c, n = seqs.model.cfg, seqs.kv.numel() // 2
+    shape = (c.n_layers, seqs.n_seq, c.n_kv)
+    return (seqs.kv[:n].view(torch.bfloat16).view(*shape, seqs.max_ctx, c.d_head),
+            seqs.kv[n:].view(torch.bfloat16).view(*shape, c.d_head, seqs.max_ctx))
+
+
+@pytest.mark.parametrize("P", [1, 63, 130, 192])
+def test_prefixes_wait_in_four_bits(P):
+    """A prompt's prefix goes into the cache, is shared there, and comes back for two sequences of another set: its rows are the
+    quantised ones, and a canvas step is the one that the same rows give when they are loaded directly."""
+    import synthetic
+    cfg = synthetic.TINY
+    w = synthetic.make_model_weights(cfg, 0, device="cuda", gain_std=0.1)
+    model = dg.dg_model_create(cfg, w)
+    one = dg.dg_seqs_create(model, 2, 512)
+    ids = synthetic.make_ids(P + 5, cfg.vocab, 1, device="cuda")
+    dg.dg_prefill(one, ids, [P, 5])
+    c = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, cfg.d_head, 12, 3, 4)
+    dg.dg_kv4_extend(c, dev([0, P, 0]))
+    dg.dg_store_prefix_kv4(one, 0, c, 1)
+    dg.dg_kv4_fork(c, dev([1]), dev([2]))
+    assert dg.dg_kv4_error(c) == 0
+    k, v = kv_views(one)
+    rows = []
+    for layer in range(cfg.n_layers):
+        want = [R.value(*R.quantise(x.double().cpu().numpy())) for x in (k[layer, 0, :, :P],
+                                                                        v[layer, 0, :, :, :P].transpose(1, 2).contiguous())]
+        for got, x in zip(blocks(c, layer, 1), want):
+            np.testing.assert_array_equal(got, x)
+        rows.append([torch.tensor(x.transpose(1, 0, 2).copy(), device="cuda").to(torch.bfloat16) for x in want])
+    back, direct = dg.dg_seqs_create(model, 2, 512), dg.dg_seqs_create(model, 2, 512)
+    for seq, slot in ((0, 1), (1, 2)):
+        dg.dg_load_prefix_kv4(back, seq, P, c, slot)
+        dg.dg_load_prefix(direct, seq, P, [r[0] for r in rows], [r[1] for r in rows])
+    assert dg.dg_kv4_error(c) == 0 and dg.dg_seqs_get_state(back)[0] == [P, P]
+    assert torch.equal(back.kv, direct.kv)
+    prm = dg.sampler_params(cfg.vocab, seed=3)
+    logits = []
+    for s in (back, direct):
+        out = torch.empty(2 * 256, cfg.vocab, device="cuda")
+        cids = torch.empty(512, dtype=torch.int32, device="cuda")
+        commit = torch.empty(512, dtype=torch.uint8, device="cuda")
+        dg.dg_canvas_init(s, prm, cids, commit)
+        dg.dg_canvas_step(s, prm, cids, commit, torch.empty(512, device="cuda"),
+                          torch.empty(2, dtype=torch.int32, device="cuda"), logits=out)
+        assert dg.dg_device_error(s) == 0
+        logits.append(out)
+    assert torch.equal(*logits)
+
+
+def test_prefixes_that_do_not_fit():
+    import synthetic
+    cfg = synthetic.TINY
+    model = dg.dg_model_create(cfg, synthetic.make_model_weights(cfg, 0, device="cuda"))
+    s = dg.dg_seqs_create(model, 1, 512)
+    dg.dg_prefill(s, synthetic.make_ids(100, cfg.vocab, 1, device="cuda"), [100])
+    c = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, cfg.d_head, 4, 2, 4)
+    dg.dg_kv4_extend(c, dev([99, 0]))
+    before, kv = c.pool.clone(), s.kv.clone()
+    dg.dg_store_prefix_kv4(s, 0, c, 0)                  # the slot has another length
+    assert dg.dg_kv4_error(c) == 8 and torch.equal(before, c.pool)
+    dg.dg_load_prefix_kv4(s, 0, 98, c, 0)
+    assert dg.dg_kv4_error(c) == 8 and torch.equal(kv, s.kv)
+    other = dg.dg_kv4_cache(cfg.n_layers + 1, cfg.n_kv, cfg.d_head, 4, 2, 4)
+    short = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, cfg.d_head, 4, 2, 1)
+    for call in (lambda: dg.dg_store_prefix_kv4(s, 1, c, 0), lambda: dg.dg_store_prefix_kv4(s, 0, c, 2),
+                 lambda: dg.dg_load_prefix_kv4(s, 0, 300, c, 0), lambda: dg.dg_load_prefix_kv4(s, 0, -1, c, 0),
+                 lambda: dg.dg_store_prefix_kv4(s, 0, other, 0), lambda: dg.dg_load_prefix_kv4(s, 0, 80, short, 0)):
+        with pytest.raises(dg.DGError):
+            call()

@@ -444,52 +444,90 @@ __device__ __forceinline__ Pieces pieces_of(const Kv4View& c, const Kv4Attn& a, 
   return p;
 }
 
-// few rows: one warp for each (sequence, row, head)
+// few rows: a CTA for each (sequence, row, head), whose warps share out the pieces (one token behind 32768 positions has 56 a
+// row: one warp walking them spent 4 us waiting for its loads)
+constexpr int kMergeWarps = 8;
 template <int DH, typename T>
-__global__ void __launch_bounds__(256) kv4_merge_few_kernel(Kv4View c, Kv4Attn a) {
+__global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_few_kernel(Kv4View c, Kv4Attn a) {
   pdl_trigger();
   pdl_wait();
   constexpr int kPer = DH / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ float tops[kMergeWarps], dens[kMergeWarps], accs[kMergeWarps][DH];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.n_q / c.n_kv;
-  const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
-  const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (at >= rows) return;
-  const int h = (int)(at % a.n_q), j = (int)(at / a.n_q % a.rows), seq = (int)(at / a.n_q / a.rows);
+  const int h = blockIdx.x % a.n_q, j = blockIdx.x / a.n_q % a.rows, seq = blockIdx.x / a.n_q / a.rows;
   const SeqView v = seq_view(c, a, seq);
   if (j >= v.n) return;
   const int r = j * G + h % G;
   const Pieces p = pieces_of<kKv4FewTile, kKv4FewStep>(c, a, seq, v, h / G, r / kKv4FewTile);
   if (p.c0 == p.c1) return;
   const size_t row = r % kKv4FewTile;
-  float top = -INFINITY;
-  for (int s = p.c0 + lane; s <= p.c1; s += 32) top = max_nan(top, a.part_lse[p.slot(s) * kKv4FewTile + row]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float acc[kPer], den = 0.f;
+  // this warp's pieces c0 + warp, c0 + warp + 8, ...: running maximum, eight at a time
+  float top = -INFINITY, den = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int s = p.c0; s <= p.c1; ++s) {
-      const size_t slot = p.slot(s) * kKv4FewTile + row;
-      const float f = fast_exp2(a.part_lse[slot] - top);
-      const float* src = static_cast<const float*>(a.part_o) + slot * DH + lane * kPer;
-      den += f;
+  for (int s0 = p.c0 + warp; s0 <= p.c1; s0 += 8 * kMergeWarps) {
+    float le[8], x[8][kPer];
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + e);
-        acc[e] += f * y.x;
-        acc[e + 1] += f * y.y;
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + k * kMergeWarps;
+      le[k] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[k][e] = 0.f;
+      if (s <= p.c1) {
+        const size_t slot = p.slot(s) * kKv4FewTile + row;
+        le[k] = a.part_lse[slot];
+        const float* src = static_cast<const float*>(a.part_o) + slot * DH + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          x[k][e] = y.x;
+          x[k][e + 1] = y.y;
+        }
       }
     }
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + lane * kPer;
+    float now = top;
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = Half<T>::pack(acc[e] * inv, acc[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[at] = (top + log2f(den)) * 0.6931471805599453f;
+    for (int k = 0; k < 8; ++k) now = max_nan(now, le[k]);
+    if (now == -INFINITY) continue;
+    const float keep = fast_exp2(top - now);
+    den *= keep;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = fast_exp2(le[k] - now);
+      den += f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += f * x[k][e];
+    }
+    top = now;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) accs[warp][lane * kPer + e] = acc[e];
+  if (lane == 0) {
+    tops[warp] = top;
+    dens[warp] = den;
+  }
+  __syncthreads();
+  for (int ch = threadIdx.x * 2; ch < DH; ch += 64 * kMergeWarps) {
+    float m = tops[0], d = 0.f, v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) m = max_nan(m, tops[w]);
+    if (m != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        const float f = fast_exp2(tops[w] - m);
+        d += f * dens[w];
+        v0 += f * accs[w][ch];
+        v1 += f * accs[w][ch + 1];
+      }
+    }
+    const float inv = d == 0.f ? 0.f : 1.f / d;
+    T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
+    *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0 * inv, v1 * inv);
+    if (a.lse && ch == 0) a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = (m + log2f(d)) * 0.6931471805599453f;
+  }
 }
 
 // many rows: a CTA for 64 group rows of a (sequence, KV head); thread = (row, pair of 8-channel chunks): loads of the
@@ -514,7 +552,7 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
   if (top != -INFINITY) {
-#pragma unroll 4
+#pragma unroll 8
     for (int s = p.c0; s <= p.c1; ++s) {
       const size_t slot = p.slot(s);
       const float f = fast_exp2(a.part_lse[slot * kKv4ManyTile + row] - top);
@@ -572,7 +610,7 @@ template <int DH, typename T>
 cudaError_t launch_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st) {
   if (few) {
     const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
-    return launch_k(kv4_merge_few_kernel<DH, T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, c, a);
+    return launch_k(kv4_merge_few_kernel<DH, T>, dim3((unsigned)rows), dim3(32 * kMergeWarps), 0, st, 1, c, a);
   }
   const dim3 grid((a.rows * (a.n_q / c.n_kv) + kMergeRows - 1) / kMergeRows, c.n_kv, c.n_seq);
   return launch_k(kv4_merge_many_kernel<DH, T>, grid, dim3(kMergeRows * DH / 16), 0, st, 1, c, a);

@@ -248,6 +248,7 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   k.o_row = a->o_row;
   k.o_head = a->o_head;
   k.n_q = a->n_q;
+  k.group = a->n_q / c->n_kv;
   k.rows = a->rows;
   k.causal = a->causal;
   k.fp16 = a->dtype == DG_DTYPE_FP16;

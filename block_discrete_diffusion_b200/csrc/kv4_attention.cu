@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   __syncwarp();
   pdl_wait();
 
-  const int G = a.n_q / c.n_kv;
+  const int G = a.group;
   int phase = 0;                // copies that each stage of the ring has seen, one bit each: its barrier's parity
   bool ok = true;
   // one piece of work
@@ -434,7 +434,7 @@ struct Pieces {
 template <int TILE, int STEP>
 __device__ __forceinline__ Pieces pieces_of(const Kv4View& c, const Kv4Attn& a, int seq, const SeqView& v, int head,
                                             int tile) {
-  const SeqWork<TILE, STEP> w(v, a.n_q / c.n_kv);
+  const SeqWork<TILE, STEP> w(v, a.group);
   const long long share = reinterpret_cast<const LineHeader*>(a.line)->share;
   const long long start = line_base(a.line)[seq] + ((long long)head * w.tiles + tile) * w.cost;
   Pieces p;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_few_kernel(Kv4View
   constexpr int kPer = DH / 32;
   __shared__ float tops[kMergeWarps], dens[kMergeWarps], accs[kMergeWarps][DH];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.n_q / c.n_kv;
+  const int G = a.group;
   const int h = blockIdx.x % a.n_q, j = blockIdx.x / a.n_q % a.rows, seq = blockIdx.x / a.n_q / a.rows;
   const SeqView v = seq_view(c, a, seq);
   if (j >= v.n) return;
@@ -537,7 +537,7 @@ template <int DH, typename T>
 __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4View c, Kv4Attn a) {
   pdl_trigger();
   pdl_wait();
-  const int G = a.n_q / c.n_kv;
+  const int G = a.group;
   const int seq = blockIdx.z, head = blockIdx.y;
   const SeqView v = seq_view(c, a, seq);
   const int r = blockIdx.x * kMergeRows + threadIdx.x % kMergeRows, chunk = threadIdx.x / kMergeRows * 2;
@@ -597,7 +597,7 @@ cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream
     if (e != cudaSuccess) return e;
   }
   if (a.cluster) {
-    const int units = (a.rows * (a.n_q / c.n_kv) + kKv4FewTile - 1) / kKv4FewTile * c.n_kv * c.n_seq;
+    const int units = (a.rows * a.group + kKv4FewTile - 1) / kKv4FewTile * c.n_kv * c.n_seq;
     return launch_k(kv4_attend_few_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(32 * kFewWarps),
                     sizeof(FewSmem<DH>), st, a.cluster, c, layer, a);
   }
@@ -612,7 +612,7 @@ cudaError_t launch_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStrea
     const size_t rows = (size_t)c.n_seq * a.rows * a.n_q;
     return launch_k(kv4_merge_few_kernel<DH, T>, dim3((unsigned)rows), dim3(32 * kMergeWarps), 0, st, 1, c, a);
   }
-  const dim3 grid((a.rows * (a.n_q / c.n_kv) + kMergeRows - 1) / kMergeRows, c.n_kv, c.n_seq);
+  const dim3 grid((a.rows * a.group + kMergeRows - 1) / kMergeRows, c.n_kv, c.n_seq);
   return launch_k(kv4_merge_many_kernel<DH, T>, grid, dim3(kMergeRows * DH / 16), 0, st, 1, c, a);
 }
 

@@ -117,7 +117,7 @@ struct Stretch {
 
   // Whole warp.  `lead`: the one warp of the grid that leaves the header and reports counts that do not fit.
   __device__ __forceinline__ Stretch(const Kv4View& c_, const Kv4Attn& a_, bool lead)
-      : c(c_), a(a_), G(a_.n_q / c_.n_kv), lane(threadIdx.x & 31), left(0), seq(c_.n_seq), unit(0), step(0),
+      : c(c_), a(a_), G(a_.group), lane(threadIdx.x & 31), left(0), seq(c_.n_seq), unit(0), step(0),
         at_begin(true) {
     long long total = 0, part, at = 0;
 #pragma unroll 1

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   const uint32_t tmem = bars->tmem;
   pdl_wait();
 
-  const int G = a.n_q / c.n_kv;
+  const int G = a.group;
   Tasks tasks{bars, err};
   Task pc;
   bool ok = true;
@@ -461,37 +461,57 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       if (steps > 0) {
         // Q to fp16 in the swizzled layout, times a power of two: dh / 8 lanes a row, so that a row is read in one
         // piece (the S products of the last piece, which read these rows, are complete: this warp has read the last S)
-        constexpr int kLanes = DH / 8, kRows = 32 / kLanes;
+        constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kN = 32 / kRows;   // kN rounds of kRows rows; kN == kLanes
         const int sub = lane % kLanes;
-        float mine = 0.f;
-        uint4 all[32 / kRows];
+        uint4 all[kN];
+        {
+          const int first = x * 128 + (warp & 3) * 32 + lane / kLanes;   // row of round 0, then kRows further each
+          int qj = (pc.row0 + first) / G, qg = (pc.row0 + first) % G;
+          const int dj = kRows / G, dg = kRows % G;
+          const T* q = static_cast<const T*>(a.q) + pc.seq * a.q_seq + (pc.head * G) * a.q_head + sub * 8;
 #pragma unroll
-        for (int i = 0; i < 32; i += kRows) {
-          const int at = x * 128 + (warp & 3) * 32 + i + lane / kLanes, R = pc.row0 + at;
-          all[i / kRows] = make_uint4(0, 0, 0, 0);
-          if (at < pc.nr)
-            all[i / kRows] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + pc.seq * a.q_seq +
-                                                             (R / G) * a.q_row + (pc.head * G + R % G) * a.q_head + sub * 8);
+          for (int i = 0; i < kN; ++i) {
+            all[i] = make_uint4(0, 0, 0, 0);
+            if (first + i * kRows < pc.nr) all[i] = *reinterpret_cast<const uint4*>(q + qj * a.q_row + qg * a.q_head);
+            qj += dj;
+            qg += dg;
+            if (qg >= G) {
+              qg -= G;
+              ++qj;
+            }
+          }
+        }
+        // largest magnitudes: kN values a lane, reduced over the kLanes lanes of a row so that lane k ends with round k's
+        float mx[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const uint32_t wd[4] = {all[i].x, all[i].y, all[i].z, all[i].w};
+          mx[i] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[i] = max3(mx[i], fabsf(Half<T>::lo(wd[e])), fabsf(Half<T>::hi(wd[e])));
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += kRows) {
-          const int row = i + lane / kLanes;
-          const uint4 raw = all[i / kRows];
-          uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-          float amax = 0.f;
+        for (int o = kN / 2; o >= 1; o /= 2) {
+          const bool upper = sub & o;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = max3(amax, fabsf(Half<T>::lo(wd[e])), fabsf(Half<T>::hi(wd[e])));
+          for (int k = 0; k < o; ++k) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? mx[k] : mx[k + o], o);
+            mx[k] = fmaxf(upper ? mx[k + o] : mx[k], other);
+          }
+        }
+        float down, up;
+        row_powers(mx[0], down, up);
 #pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          float down, up;
-          row_powers(amax, down, up);
+        for (int i = 0; i < kN; ++i) {
+          const int row = i * kRows + lane / kLanes;
+          const float d = __shfl_sync(0xffffffffu, down, lane - sub + i);
+          uint32_t wd[4] = {all[i].x, all[i].y, all[i].z, all[i].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) wd[e] = pack_f16x2(Half<T>::lo(wd[e]) * down, Half<T>::hi(wd[e]) * down);
+          for (int e = 0; e < 4; ++e) wd[e] = pack_f16x2(Half<T>::lo(wd[e]) * d, Half<T>::hi(wd[e]) * d);
           *reinterpret_cast<uint4*>(qtile + (sub / 8) * 16384 + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
               make_uint4(wd[0], wd[1], wd[2], wd[3]);
-          const float u = __shfl_sync(0xffffffffu, up, (lane % kRows) * kLanes);   // of row i + lane % kRows
-          if (lane / kRows == i / kRows) mine = u;
         }
+        const float mine = __shfl_sync(0xffffffffu, up, (lane % kRows) * kLanes + lane / kRows);   // of row `lane`
         sl2 = fmaxf(a.scale * 1.4426950408889634f * mine, 1e-44f);   // (above 0, so that -inf stays -inf)
         fence_proxy_async_smem();
         __syncwarp();

@@ -48,6 +48,7 @@ struct Kv4Attn {
   const int32_t* n_rows;
   long long q_seq, q_row, q_head, o_seq, o_row, o_head;
   int n_q, rows, causal, fp16;
+  int group;               // query heads of a KV head
   float scale;
   int cluster;             // few rows: CTAs of a unit's cluster (the rows are joined there), 0: divide the line
   int n_ctas;              // CTAs among which the work is divided

@@ -124,6 +124,13 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     p.row_bytes = 4 * (size_t)c->d_head;
   } else {
     p.n_ctas = sms;                                // one CTA holds an SM
+    // Clusters here too where all units' run at once and none is long (see above).  Eight CTAs of a GPC's SMs at most, and
+    // fewer clusters than SMs / size would give: with 16 clusters of 8 the last ones waited (2304 positions, one canvas:
+    // 36.9 us; 16 clusters of 4 22.6 us, the line 23.8 us; 600 positions 30.5, 15.7, 19.6 us).
+    const long long many = (group_rows + kKv4ManyTile - 1) / kKv4ManyTile * c->n_kv * c->n_seq;
+    int m = many <= sms ? kKv4MaxManyCluster : 0;
+    while (m > 0 && many > kv4_many_clusters(c->d_head, m)) --m;
+    if (m > 0 && c->max_pages <= (c->n_seq == 1 ? 24 : 16) * m) p.cluster = m;
     p.min_share = 1;
     p.tile = kKv4ManyTile;
     p.row_bytes = 2 * (size_t)c->d_head;

@@ -47,17 +47,6 @@ struct FewSmem {
   float m[kFewWarps][kKv4FewTile], l[kFewWarps][kKv4FewTile];
 };
 
-__device__ __forceinline__ float2 dsmem_ld_f2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float dsmem_ld_f1(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // Cluster: grid (unit, 1, CTA of the unit's cluster); else the CTAs divide the line.
 template <int DH, typename T, bool Cluster>
 __global__ void __launch_bounds__(32 * kFewWarps)

@@ -181,6 +181,17 @@ struct Stretch {
   }
 };
 
+__device__ __forceinline__ float2 dsmem_ld_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float dsmem_ld_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // the workspace slot of a piece that is part of a unit
 __device__ __forceinline__ size_t slot_of(const Piece& p) { return 2 * (size_t)blockIdx.x + (p.first ? 0 : 1); }
 

@@ -16,6 +16,9 @@
 // P as the tensor core's operand in TMEM and not in shared memory takes 128 KB off the 384 KB that 128 positions
 // cost there; the blocks come by bulk copies because loads into registers were waited for by each tile's proxy fence.
 //
+// A call whose units fit the SMs in clusters runs one for each unit: its CTAs leave their rows in shared memory, where
+// each joins a share of them through distributed shared memory, and the second launch falls away.
+//
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
 // positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in the same
 // order, which only renames registers.  The running maximum is lazy: O and the sum are rescaled when a row's
@@ -31,16 +34,18 @@ namespace {
 constexpr int kManyThreads = 512;
 // Registers a thread after the split of the launch's 4 x 128: two softmax groups, the dequantisers, the issuers.
 constexpr int kRegsSoftmax = 152, kRegsDequant = 120, kRegsIssue = 88;
-static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * 128, "register split above what the CTA was launched with");
+constexpr int kRegsLaunch = 128;
+static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * kRegsLaunch, "register split above what the CTA was launched with");
 constexpr int kRing = 8;       // fp16 tiles of 64 positions
 constexpr int kRaw = 3;        // pages' blocks
 constexpr float kLazy = 8.f;   // log2 units
+constexpr int kMaxManyCluster = kKv4MaxManyCluster;
 
 template <int DH>
 struct ManySmem {
   static constexpr uint32_t kQ = 128u * DH * 2u;       // a Q tile
   static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
-  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640;
+  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -135,7 +140,8 @@ struct Tasks {
   }
 };
 
-template <int DH, typename T>
+// Cluster: grid (unit, 1, CTA of the unit's cluster); else the CTAs divide the line.
+template <int DH, typename T, bool Cluster>
 __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4View c, int layer, Kv4Attn a) {
   using F = Kv4<DH>;
   using C = ManySmem<DH>;
@@ -145,6 +151,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   uint8_t* kv_s = q_s + 2 * C::kQ;
   uint8_t* raw_s = kv_s + kRing * C::kTile;
   ManyBars* bars = reinterpret_cast<ManyBars*>(raw_s + kRaw * F::kBytes);
+  float* lse_s = reinterpret_cast<float*>(raw_s + kRaw * F::kBytes + 640);   // a cluster's CTA: its rows' lse
   static_assert(sizeof(ManyBars) <= 640, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = c.head + KV4_WORD_WAIT;
@@ -313,29 +320,52 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         }
       }
     }
+    if constexpr (Cluster) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 13) {
       // ------------------------------ pieces ------------------------------
-      Stretch<kKv4ManyTile, kKv4ManyStep> stretch(c, a, blockIdx.x == 0);
-      Piece p;
-      for (uint32_t i = 0;; ++i) {
-        const int k = i % kTasks;
-        const bool more = stretch.next(p);
-        if (!warp_wait(&bars->task_empty[k], ((i / kTasks) & 1) ^ 1, err)) break;
+      auto task_of = [&](const Piece& p) {
+        const int row0 = p.tile * kKv4ManyTile, nr = min(kKv4ManyTile, p.v.n * G - row0);
+        const int limit = row_limit(p.v, (row0 + nr - 1) / G, a.causal);   // the last row sees the most
+        const int steps = max(0, min((limit + kKv4ManyStep - 1) / kKv4ManyStep, p.s1) - p.s0);
+        return Task{p.seq, p.head, row0, nr, p.s0, steps, p.v.len, p.v.n, p.whole(), (int)slot_of(p)};
+      };
+      const Task none{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
+      if constexpr (Cluster) {
+        // one piece: this CTA's share of the unit's pages; the unit may have no rows
+        const int tiles = (a.rows * G + kKv4ManyTile - 1) / kKv4ManyTile, n = gridDim.z;
+        Piece p;
+        p.tile = blockIdx.x % tiles;
+        p.head = blockIdx.x / tiles % c.n_kv;
+        p.seq = blockIdx.x / tiles / c.n_kv;
+        p.v = seq_view(c, a, p.seq, lane == 0);
+        const int pages = (p.v.len + kPage - 1) / kPage, per = (pages + n - 1) / n;
+        p.cost = max(1, pages);
+        p.s0 = n == 1 ? 0 : min(pages, (int)blockIdx.z * per);
+        p.s1 = n == 1 ? p.cost : min(pages, p.s0 + per);
+        p.first = true;
         if (lane == 0) {
-          Task t{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
-          if (more) {
-            const int row0 = p.tile * kKv4ManyTile, nr = min(kKv4ManyTile, p.v.n * G - row0);
-            const int limit = row_limit(p.v, (row0 + nr - 1) / G, a.causal);   // the last row sees the most
-            const int steps = max(0, min((limit + kKv4ManyStep - 1) / kKv4ManyStep, p.s1) - p.s0);
-            t = Task{p.seq, p.head, row0, nr, p.s0, steps, p.v.len, p.v.n, p.whole(), (int)slot_of(p)};
-          }
-          bars->task[k] = t;
-          mbar_arrive(&bars->task_full[k]);
+          const bool some = p.tile * kKv4ManyTile < p.v.n * G;
+          bars->task[0] = some ? task_of(p) : none;
+          bars->task[1] = none;
+          mbar_arrive(&bars->task_full[0]);
+          mbar_arrive(&bars->task_full[1]);
         }
-        __syncwarp();
-        if (!more) break;
+      } else {
+        Stretch<kKv4ManyTile, kKv4ManyStep> stretch(c, a, blockIdx.x == 0);
+        Piece p;
+        for (uint32_t i = 0;; ++i) {
+          const int k = i % kTasks;
+          const bool more = stretch.next(p);
+          if (!warp_wait(&bars->task_empty[k], ((i / kTasks) & 1) ^ 1, err)) break;
+          if (lane == 0) {
+            bars->task[k] = more ? task_of(p) : none;
+            mbar_arrive(&bars->task_full[k]);
+          }
+          __syncwarp();
+          if (!more) break;
+        }
       }
     } else if (warp == 14) {
       // ------------------------------ blocks ------------------------------
@@ -441,6 +471,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         item += 2 * steps;
       }
     }
+    __syncwarp();
+    if constexpr (Cluster) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------ softmax ------------------------------
@@ -602,7 +634,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
-        if (valid && ok) {
+        if (Cluster && gridDim.z > 1) {
+          // into this tile's Q, whose last products are complete: row r's 16-byte chunks, swizzled for the banks
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(q_s + x * C::kQ + r * (2 * DH) + ((((cb + e) / 8) ^ (r & 7)) << 4)) =
+                make_uint4(pack_f16x2(o[e], o[e + 1]), pack_f16x2(o[e + 2], o[e + 3]),
+                           pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
+        } else if (valid && ok) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             if (pc.whole)
@@ -616,7 +655,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           }
         }
       }
-      if (valid && ok) {
+      if (Cluster && gridDim.z > 1) {
+        lse_s[x * 128 + r] = lse2;
+      } else if (valid && ok) {
         if (!pc.whole)
           a.part_lse[at] = lse2;
         else if (a.lse)
@@ -624,25 +665,118 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       }
       tc_fence_before();   // O is read before the next piece's products overwrite it (they wait for p_ready)
     }
+    // (a cluster's CTA goes on with all its warps: everyone back to the registers of the launch)
+    if constexpr (Cluster) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 12) tmem_dealloc(tmem, 512);
+  if (Cluster && gridDim.z > 1) {
+    // every CTA of the cluster joins its share of the unit's rows, a thread for 8 channels of a row at a time
+    cluster_sync();
+    const int tiles = (a.rows * G + kKv4ManyTile - 1) / kKv4ManyTile, n = gridDim.z;
+    const int tile = blockIdx.x % tiles, head = blockIdx.x / tiles % c.n_kv, seq = blockIdx.x / tiles / c.n_kv;
+    const int nr = min(kKv4ManyTile, seq_view(c, a, seq).n * G - tile * kKv4ManyTile);
+    const int per = (nr + n - 1) / n;   // rows of a CTA (nr <= 0: none)
+    constexpr int kChunks = DH / 8;
+    const uint32_t q_addr = smem_u32(q_s), lse_addr = smem_u32(lse_s);
+    for (int i = threadIdx.x; i < per * kChunks; i += kManyThreads) {
+      const int at = blockIdx.z * per + i / kChunks, chunk = i % kChunks;
+      if (at >= nr) break;
+      const int r = at & 127;
+      const uint32_t off = q_addr + (at >> 7) * C::kQ + r * (2 * DH) + ((chunk ^ (r & 7)) << 4);
+      float le[kMaxManyCluster], top = -INFINITY;
+      float4 x[kMaxManyCluster];
+#pragma unroll
+      for (int k = 0; k < kMaxManyCluster; ++k) {
+        le[k] = k < n ? dsmem_ld_f1(dsmem_map(lse_addr + 4 * at, k)) : -INFINITY;
+        x[k] = k < n ? dsmem_ld_f4(dsmem_map(off, k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        top = max_nan(top, le[k]);
+      }
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, den = 0.f;
+      if (top != -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < kMaxManyCluster; ++k) {
+          const float f = k < n ? fast_exp2(le[k] - top) : 0.f;
+          const uint32_t w[4] = {__float_as_uint(x[k].x), __float_as_uint(x[k].y), __float_as_uint(x[k].z),
+                                 __float_as_uint(x[k].w)};
+          den += f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[2 * e] += f * Half<__half>::lo(w[e]);
+            acc[2 * e + 1] += f * Half<__half>::hi(w[e]);
+          }
+        }
+      }
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      const int rr = tile * kKv4ManyTile + at, j = rr / G, h = head * G + rr % G;
+      T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * 8;
+      *reinterpret_cast<uint4*>(dst) =
+          make_uint4(Half<T>::pack(acc[0] * inv, acc[1] * inv), Half<T>::pack(acc[2] * inv, acc[3] * inv),
+                     Half<T>::pack(acc[4] * inv, acc[5] * inv), Half<T>::pack(acc[6] * inv, acc[7] * inv));
+      if (a.lse && chunk == 0)
+        a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = (top + log2f(den)) * 0.6931471805599453f;
+    }
+    cluster_sync();   // this CTA's rows stay until all have read them
+  }
+}
+
+template <int DH, typename T>
+cudaError_t prepare_many() {
+  static unsigned long long done = 0;
+  if (!first_on_device(&done)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
+}
+
+template <int DH>
+int clusters_at_once(int n) {
+  if (prepare_many<DH, __nv_bfloat16>() != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, n);
+  cfg.blockDim = dim3(kManyThreads);
+  cfg.dynamicSmemBytes = ManySmem<DH>::kBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = n;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int count = 0;
+  return cudaOccupancyMaxActiveClusters(&count, kv4_attend_many_kernel<DH, __nv_bfloat16, true>, &cfg) == cudaSuccess
+             ? count
+             : 0;
 }
 
 template <int DH, typename T>
 cudaError_t launch_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st) {
-  static unsigned long long done = 0;
-  if (first_on_device(&done)) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
-    if (e != cudaSuccess) return e;
+  constexpr int kBytes = (int)ManySmem<DH>::kBytes;
+  const cudaError_t e = prepare_many<DH, T>();
+  if (e != cudaSuccess) return e;
+  if (a.cluster) {
+    const int units = (a.rows * a.group + kKv4ManyTile - 1) / kKv4ManyTile * c.n_kv * c.n_seq;
+    return launch_k(kv4_attend_many_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(kManyThreads), kBytes, st,
+                    a.cluster, c, layer, a);
   }
-  return launch_k(kv4_attend_many_kernel<DH, T>, dim3(a.n_ctas), dim3(kManyThreads), ManySmem<DH>::kBytes, st, 1, c,
-                  layer, a);
+  return launch_k(kv4_attend_many_kernel<DH, T, false>, dim3(a.n_ctas), dim3(kManyThreads), kBytes, st, 1, c, layer, a);
 }
 
 }  // namespace
+
+int kv4_many_clusters(int dh, int n) {
+  static int known[2][64][kMaxManyCluster + 1];   // by head size and device: count + 1, 0 where not asked for yet
+  int dev = 0;
+  if (n < 1 || n > kMaxManyCluster || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int v = __atomic_load_n(&known[dh == 128][dev][n], __ATOMIC_RELAXED);
+  if (v == 0) {
+    v = (dh == 128 ? clusters_at_once<128>(n) : clusters_at_once<64>(n)) + 1;
+    __atomic_store_n(&known[dh == 128][dev][n], v, __ATOMIC_RELAXED);
+  }
+  return v - 1;
+}
 
 cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st) {
   if (c.dh == 128)

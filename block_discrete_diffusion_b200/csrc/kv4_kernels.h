@@ -50,7 +50,7 @@ struct Kv4Attn {
   int n_q, rows, causal, fp16;
   int group;               // query heads of a KV head
   float scale;
-  int cluster;             // few rows: CTAs of a unit's cluster (the rows are joined there), 0: divide the line
+  int cluster;             // CTAs of a unit's cluster (the rows are joined there), 0: divide the line
   int n_ctas;              // CTAs among which the work is divided
   int min_share;           // key steps that a CTA takes at least
   void* line;              // header of the division: 16 bytes and n_seq words of 8 bytes
@@ -61,9 +61,11 @@ struct Kv4Attn {
 // Few rows of a KV head (single tokens): tiles of 8 rows, steps of one page, mma.sync on fragments dequantised in
 // registers.  Many rows (canvases, prompt chunks): tiles of 256 rows, steps of one page, tcgen05.
 constexpr int kKv4FewTile = 8, kKv4FewStep = 64, kKv4MaxCluster = 16;
-constexpr int kKv4ManyTile = 256, kKv4ManyStep = 64;
+constexpr int kKv4ManyTile = 256, kKv4ManyStep = 64, kKv4MaxManyCluster = 8;
 cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
+// How many clusters of n CTAs of the many-rows form the current device runs at once (0 without a device).
+int kv4_many_clusters(int dh, int n);
 cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaStream_t st);
 
 // the checks of a cache's shape and buffers that every entry point makes, and its device view

@@ -602,3 +602,12 @@ def test_prefixes_that_do_not_fit():
                  lambda: dg.dg_store_prefix_kv4(s, 0, other, 0), lambda: dg.dg_load_prefix_kv4(s, 0, 80, short, 0)):
         with pytest.raises(dg.DGError):
             call()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("n_q,n_kv,dh,dtype", [(16, 8, 128, BF16), (32, 8, 64, FP16)])
+@pytest.mark.parametrize("lens,rows", [([700], None), ([1], None), ([2900], None), ([0, 300], [3, 256]), ([513, 40], [256, 0]),
+                                       ([300, 1000, 5, 256, 64, 0, 700, 128], [256, 200, 129, 1, 0, 7, 128, 64])], ids=str)
+def test_canvases_in_clusters(lens, rows, causal, n_q, n_kv, dh, dtype):
+    """Canvases of one to eight sequences, which are shared out among clusters of six, four, two and single CTAs."""
+    attend(make(n_kv, dh, lens), n_q, 256, dtype, rows=rows, causal=causal)

@@ -575,16 +575,17 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
 template <int DH, typename T>
 cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st) {
   static unsigned long long done = 0;
-  if (first_on_device(&done)) {
+  const cudaError_t e = once_per_device(&done, [] {
     cudaError_t e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, false>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(FewSmem<DH>));
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                sizeof(FewSmem<DH>));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+    return e != cudaSuccess
+               ? e
+               : cudaFuncSetAttribute(kv4_attend_few_kernel<DH, T, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return e;
   if (a.cluster) {
     const int units = (a.rows * a.group + kKv4FewTile - 1) / kKv4FewTile * c.n_kv * c.n_seq;
     return launch_k(kv4_attend_few_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(32 * kFewWarps),

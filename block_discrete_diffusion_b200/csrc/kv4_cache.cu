@@ -18,13 +18,6 @@
 
 namespace dg {
 
-bool first_on_device(unsigned long long* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return true;
-  const unsigned long long bit = 1ull << dev;
-  return !(__atomic_fetch_or(done, bit, __ATOMIC_RELAXED) & bit);
-}
-
 namespace {
 
 // 8 elements (16 bytes) of a row

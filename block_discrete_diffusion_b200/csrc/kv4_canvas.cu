@@ -724,12 +724,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
 template <int DH, typename T>
 cudaError_t prepare_many() {
   static unsigned long long done = 0;
-  if (!first_on_device(&done)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
+  return once_per_device(&done, [] {
+    const cudaError_t e = cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, false>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ManySmem<DH>::kBytes);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(kv4_attend_many_kernel<DH, T, true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)ManySmem<DH>::kBytes);
+  });
 }
 
 template <int DH>
@@ -746,9 +748,10 @@ int clusters_at_once(int n) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int count = 0;
-  return cudaOccupancyMaxActiveClusters(&count, kv4_attend_many_kernel<DH, __nv_bfloat16, true>, &cfg) == cudaSuccess
-             ? count
-             : 0;
+  if (cudaOccupancyMaxActiveClusters(&count, kv4_attend_many_kernel<DH, __nv_bfloat16, true>, &cfg) == cudaSuccess)
+    return count;
+  cudaGetLastError();   // (a size the device does not take is an answer, not an error of the call)
+  return 0;
 }
 
 template <int DH, typename T>

@@ -72,7 +72,18 @@ cudaError_t kv4_attend_merge(const Kv4View& c, const Kv4Attn& a, bool few, cudaS
 dg_status kv4_check_cache(const char* fn, const dg_kv4_cache* c);
 Kv4View kv4_view(const dg_kv4_cache* c);
 
-// kernel attributes are per device: true the first time `done` (one per kernel) meets the current device
-bool first_on_device(unsigned long long* done);
+// Kernel attributes are per device: `set` (which may run twice where two threads come first at once) runs until it has
+// succeeded on the current device; `done` is the kernel's own word of devices.
+template <typename F>
+cudaError_t once_per_device(unsigned long long* done, F set) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (__atomic_load_n(done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
+  e = set();
+  if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELEASE);
+  return e;
+}
 
 }  // namespace dg

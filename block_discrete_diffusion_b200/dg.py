@@ -439,6 +439,8 @@ def _kv4_tensor(cache, t, shape, what, dtype=None):
     s = t.stride()
     if s[3] != 1:
         raise ValueError(f"{what}: channels must be contiguous")
+    if (s[0] | s[1] | s[2]) & 7:   # the stride of a dimension of one says nothing
+        s = tuple(0 if n == 1 else k for n, k in zip(shape, s))
     return code, s
 
 

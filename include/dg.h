@@ -344,7 +344,7 @@ dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, vo
  * cache); causal = 1: row j is position len - n + j and sees itself and what comes before (a prompt chunk,
  * a single token).  A row that sees nothing is 0 with lse -inf.  Query head h reads KV head h / (n_q / n_kv).
  * Element (s, j, h, c) of q lies at q_seq * s + q_row * j + q_head * h + c elements (strides multiples of 8, rows
- * 16-byte aligned), out likewise; both of type dtype.  lse (nullable): fp32 [n_seq][rows][n_q], the natural
+ * 16-byte aligned), out likewise; both of type dtype; out may be q.  lse (nullable): fp32 [n_seq][rows][n_q], the natural
  * logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The
  * work is divided among the SMs on the device, by the lengths that it finds there.  NaN and infinities: stale
  * contents behind a sequence's end never matter; a NaN among its cached values reaches every row of the call that

@@ -611,3 +611,57 @@ def test_prefixes_that_do_not_fit():
 def test_canvases_in_clusters(lens, rows, causal, n_q, n_kv, dh, dtype):
     """Canvases of one to eight sequences, which are shared out among clusters of six, four, two and single CTAs."""
     attend(make(n_kv, dh, lens), n_q, 256, dtype, rows=rows, causal=causal)
+
+
+def test_dimensions_of_one_may_have_any_stride():
+    c = make(1, 64, [70])
+    q = torch.randn((1, 1, 1, 64), device="cuda").to(BF16)
+    odd = q.as_strided((1, 1, 1, 64), (3, 5, 7, 1))
+    outs = []
+    for x in (q, odd):
+        out = torch.empty_like(q)
+        ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 1, 1), dtype=torch.uint8, device="cuda")
+        dg.dg_kv4_attend(c, 0, x, out, ws)
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("T,table", [(1, None), (1, 3000), (256, None), (256, 3000)])
+def test_output_over_the_queries(T, table):
+    """The rows may be written over the queries that they come from."""
+    c = make(8, 128, [900, 77], max_pages=table)
+    q = torch.randn((2, T, 16, 128), device="cuda").to(BF16)
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 16, T), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    dg.dg_kv4_attend(c, 0, q, out, ws)
+    dg.dg_kv4_attend(c, 0, q, q, ws)
+    assert torch.equal(out, q)
+
+
+@pytest.mark.parametrize("T", [1, 64, 256])
+def test_captured_attention_is_repeatable_beside_another_stream(T):
+    """Replays of a captured call give the same bits while another cache's calls run on another stream."""
+    c, other = make(8, 128, [2000, 130], max_pages=3000), make(8, 128, [4000], seed=9)
+    q = torch.randn((2, T, 16, 128), device="cuda").to(BF16)
+    q2 = torch.randn((1, T, 16, 128), device="cuda").to(BF16)
+    out, first, out2 = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q2)
+    ws, ws2 = (torch.empty(dg.dg_kv4_attend_workspace_bytes(x, 16, T), dtype=torch.uint8, device="cuda") for x in (c, other))
+    dg.dg_kv4_attend(c, 0, q, first, ws)
+    dg.dg_kv4_attend(other, 0, q2, out2, ws2)
+    want2 = out2.clone()
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            dg.dg_kv4_attend(c, 0, q, out, ws)
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            out.zero_()
+            graph.replay()
+        with torch.cuda.stream(s2):
+            out2.zero_()
+            dg.dg_kv4_attend(other, 0, q2, out2, ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, first) and torch.equal(out2, want2)
+    assert dg.dg_kv4_error(c) == 0 and dg.dg_kv4_error(other) == 0

@@ -134,3 +134,30 @@ def test_attend_refused(lib, kw):
     assert lib.dg_kv4_attend(ctypes.byref(cache()), kw.get("layer", 0), ctypes.byref(attn), kw.get("ws", 4096),
                              kw.get("ws_bytes", 1 << 40), None) == want
     assert b"dg_kv4_attend" in lib.dg_last_error()
+
+
+def test_binding_structs_match_the_header_layout(tmp_path):
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no host C compiler")
+    structs = {"dg_kv4_cache": dg.dg_kv4_cache_t, "dg_kv4_rows": dg.dg_kv4_rows, "dg_kv4_attn": dg.dg_kv4_attn}
+    lines = ['#include <stdio.h>', '#include <stddef.h>', '#include "dg.h"', "int main(void) {"]
+    for name, s in structs.items():
+        lines.append(f'  printf("{name} size %zu\\n", sizeof({name}));')
+        lines += [f'  printf("{name} {f} %zu\\n", offsetof({name}, {f}));' for f, _ in s._fields_]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.run([cc, "-std=c99", "-I", build.INCLUDE, str(src), "-o", str(exe)], check=True)
+    for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines():
+        name, field, value = line.split()
+        s = structs[name]
+        assert int(value) == (ctypes.sizeof(s) if field == "size" else getattr(s, field).offset), line
+
+
+def test_prefix_calls_refused(lib):
+    c = cache()
+    assert lib.dg_store_prefix_kv4(None, 0, ctypes.byref(c), 0) == dg.DG_ERR_INVALID_ARG
+    assert lib.dg_load_prefix_kv4(None, 0, 1, ctypes.byref(c), 0) == dg.DG_ERR_INVALID_ARG
+    assert b"dg_load_prefix_kv4" in lib.dg_last_error()

@@ -133,7 +133,7 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     if (m > 0 && c->max_pages <= (c->n_seq == 1 ? 24 : 16) * m) p.cluster = m;
     p.min_share = 1;
     p.tile = kKv4ManyTile;
-    p.row_bytes = 2 * (size_t)c->d_head;
+    p.row_bytes = 4 * (size_t)c->d_head;           // (parts for a bf16 output take half of it)
   }
   return p;
 }

@@ -526,6 +526,7 @@ template <int DH, typename T>
 __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4View c, Kv4Attn a) {
   pdl_trigger();
   pdl_wait();
+  constexpr int kPer = kPartPer<T>;
   const int G = a.group;
   const int seq = blockIdx.z, head = blockIdx.y;
   const SeqView v = seq_view(c, a, seq);
@@ -541,21 +542,25 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
   if (top != -INFINITY) {
-#pragma unroll 8
+#pragma unroll 4
     for (int s = p.c0; s <= p.c1; ++s) {
       const size_t slot = p.slot(s);
       const float f = fast_exp2(a.part_lse[slot * kKv4ManyTile + row] - top);
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __half*>(a.part_o) + slot * kKv4ManyTile * DH) +
-                         chunk * kKv4ManyTile + row;
+      const uint4* src = static_cast<const uint4*>(a.part_o) +
+                         (slot * (DH / kPer) + (size_t)chunk * (8 / kPer)) * kKv4ManyTile + row;
       den += f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 16 / kPer; ++u) {
         const uint4 y = src[u * kKv4ManyTile];
         const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          acc[8 * u + 2 * e] += f * Half<__half>::lo(w[e]);
-          acc[8 * u + 2 * e + 1] += f * Half<__half>::hi(w[e]);
+          if constexpr (kPer == 4) {
+            acc[4 * u + e] += f * __uint_as_float(w[e]);
+          } else {
+            acc[8 * u + 2 * e] += f * Half<__half>::lo(w[e]);
+            acc[8 * u + 2 * e + 1] += f * Half<__half>::hi(w[e]);
+          }
         }
       }
     }

@@ -9,6 +9,8 @@
 // number of splits for each sequence left them waiting for the longest one.
 #pragma once
 
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "kv4_kernels.h"
 
@@ -191,6 +193,10 @@ __device__ __forceinline__ float dsmem_ld_f1(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+
+// Channels in a 16-byte chunk of a part of the many-rows form: fp16 for a bf16 output, fp32 for an fp16 one.
+template <typename T>
+constexpr int kPartPer = std::is_same<T, __half>::value ? 4 : 8;
 
 // the workspace slot of a piece that is part of a unit
 __device__ __forceinline__ size_t slot_of(const Piece& p) { return 2 * (size_t)blockIdx.x + (p.first ? 0 : 1); }

@@ -47,6 +47,7 @@ struct ManySmem {
   static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
   static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024;
   static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(kRing * kTile == 256u * DH * 4u, "the ring holds a CTA's rows in fp32");
 };
 
 // A piece of work as the roles need it.
@@ -623,10 +624,23 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const float lse2 = some ? m_used + log2f(l) : -INFINITY;
       T* dst = static_cast<T*>(a.out) + pc.seq * a.o_seq + j * a.o_row + h * a.o_head;
       const size_t at = (size_t)pc.slot * kKv4ManyTile + x * 128 + r;
-      // a part in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; 16-byte chunks of the
-      // tile's rows side by side, so that a warp's stores and the merge's loads are contiguous
-      uint4* part = reinterpret_cast<uint4*>(static_cast<__half*>(a.part_o) + (size_t)pc.slot * kKv4ManyTile * DH) +
-                    x * 128 + r;
+      // A part for a bf16 output in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; for an fp16
+      // output, whose own rounding that is, in fp32.  16-byte chunks of the tile's rows lie side by side, so that a
+      // warp's stores and the merge's loads are contiguous
+      constexpr int kPer = kPartPer<T>;   // channels of a chunk
+      auto chunk_of = [](const float(&o)[32], int e) {
+        if constexpr (kPer == 4)
+          return make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                            __float_as_uint(o[e + 3]));
+        else
+          return make_uint4(pack_f16x2(o[e], o[e + 1]), pack_f16x2(o[e + 2], o[e + 3]),
+                            pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
+      };
+      uint4* part = static_cast<uint4*>(a.part_o) + (size_t)pc.slot * kKv4ManyTile * (DH / kPer) + x * 128 + r;
+      if (Cluster && gridDim.z > 1) {
+        // the tiles' buffers become the CTA's rows once both tiles' products are complete
+        asm volatile("bar.sync 1, %0;" ::"r"(pc.nr > 128 ? 256 : 128) : "memory");
+      }
 #pragma unroll
       for (int cb = 0; cb < DH; cb += 32) {
         float o[32];
@@ -635,23 +649,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
         if (Cluster && gridDim.z > 1) {
-          // into this tile's Q, whose last products are complete: row r's 16-byte chunks, swizzled for the banks
+          // row r's 16-byte chunks, swizzled for the banks
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(q_s + x * C::kQ + r * (2 * DH) + ((((cb + e) / 8) ^ (r & 7)) << 4)) =
-                make_uint4(pack_f16x2(o[e], o[e + 1]), pack_f16x2(o[e + 2], o[e + 3]),
-                           pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
+          for (int e = 0; e < 32; e += kPer)
+            *reinterpret_cast<uint4*>(kv_s + (x * 128 + r) * (16 * DH / kPer) +
+                                      ((((cb + e) / kPer) ^ (r & 7)) << 4)) = chunk_of(o, e);
         } else if (valid && ok) {
+          if (pc.whole) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (pc.whole)
+            for (int e = 0; e < 32; e += 8)
               *reinterpret_cast<uint4*>(dst + cb + e) =
                   make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
                              Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
-            else
-              part[(cb + e) / 8 * kKv4ManyTile] =
-                  make_uint4(pack_f16x2(o[e], o[e + 1]), pack_f16x2(o[e + 2], o[e + 3]),
-                             pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += kPer) part[(cb + e) / kPer * kKv4ManyTile] = chunk_of(o, e);
           }
         }
       }
@@ -672,19 +684,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   __syncthreads();
   if (warp == 12) tmem_dealloc(tmem, 512);
   if (Cluster && gridDim.z > 1) {
-    // every CTA of the cluster joins its share of the unit's rows, a thread for 8 channels of a row at a time
+    // every CTA of the cluster joins its share of the unit's rows, a thread for a 16-byte chunk at a time
     cluster_sync();
     const int tiles = (a.rows * G + kKv4ManyTile - 1) / kKv4ManyTile, n = gridDim.z;
     const int tile = blockIdx.x % tiles, head = blockIdx.x / tiles % c.n_kv, seq = blockIdx.x / tiles / c.n_kv;
     const int nr = min(kKv4ManyTile, seq_view(c, a, seq).n * G - tile * kKv4ManyTile);
     const int per = (nr + n - 1) / n;   // rows of a CTA (nr <= 0: none)
-    constexpr int kChunks = DH / 8;
-    const uint32_t q_addr = smem_u32(q_s), lse_addr = smem_u32(lse_s);
+    constexpr int kPer = kPartPer<T>, kChunks = DH / kPer;
+    const uint32_t o_addr = smem_u32(kv_s), lse_addr = smem_u32(lse_s);
     for (int i = threadIdx.x; i < per * kChunks; i += kManyThreads) {
       const int at = blockIdx.z * per + i / kChunks, chunk = i % kChunks;
       if (at >= nr) break;
-      const int r = at & 127;
-      const uint32_t off = q_addr + (at >> 7) * C::kQ + r * (2 * DH) + ((chunk ^ (r & 7)) << 4);
+      const uint32_t off = o_addr + (at * kChunks + (chunk ^ (at & 7))) * 16;
       float le[kMaxManyCluster], top = -INFINITY;
       float4 x[kMaxManyCluster];
 #pragma unroll
@@ -693,27 +704,33 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         x[k] = k < n ? dsmem_ld_f4(dsmem_map(off, k)) : make_float4(0.f, 0.f, 0.f, 0.f);
         top = max_nan(top, le[k]);
       }
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, den = 0.f;
+      float acc[kPer], den = 0.f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
       if (top != -INFINITY) {
 #pragma unroll
         for (int k = 0; k < kMaxManyCluster; ++k) {
           const float f = k < n ? fast_exp2(le[k] - top) : 0.f;
-          const uint32_t w[4] = {__float_as_uint(x[k].x), __float_as_uint(x[k].y), __float_as_uint(x[k].z),
-                                 __float_as_uint(x[k].w)};
+          const float w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           den += f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc[2 * e] += f * Half<__half>::lo(w[e]);
-            acc[2 * e + 1] += f * Half<__half>::hi(w[e]);
+            if constexpr (kPer == 4) {
+              acc[e] += f * w[e];
+            } else {
+              acc[2 * e] += f * Half<__half>::lo(__float_as_uint(w[e]));
+              acc[2 * e + 1] += f * Half<__half>::hi(__float_as_uint(w[e]));
+            }
           }
         }
       }
       const float inv = den == 0.f ? 0.f : 1.f / den;
       const int rr = tile * kKv4ManyTile + at, j = rr / G, h = head * G + rr % G;
-      T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * 8;
-      *reinterpret_cast<uint4*>(dst) =
-          make_uint4(Half<T>::pack(acc[0] * inv, acc[1] * inv), Half<T>::pack(acc[2] * inv, acc[3] * inv),
-                     Half<T>::pack(acc[4] * inv, acc[5] * inv), Half<T>::pack(acc[6] * inv, acc[7] * inv));
+      T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 4)
+        *reinterpret_cast<uint2*>(dst + e) = make_uint2(Half<T>::pack(acc[e] * inv, acc[e + 1] * inv),
+                                                        Half<T>::pack(acc[e + 2] * inv, acc[e + 3] * inv));
       if (a.lse && chunk == 0)
         a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = (top + log2f(den)) * 0.6931471805599453f;
     }

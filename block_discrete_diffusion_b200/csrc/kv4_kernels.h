@@ -54,7 +54,8 @@ struct Kv4Attn {
   int n_ctas;              // CTAs among which the work is divided
   int min_share;           // key steps that a CTA takes at least
   void* line;              // header of the division: 16 bytes and n_seq words of 8 bytes
-  void* part_o;            // normalised; few rows: fp32 [2 n_ctas][tile][dh]; many: fp16 [2 n_ctas][dh / 8][tile][8]
+  void* part_o;            // normalised; few rows: fp32 [2 n_ctas][tile][dh]; many: 16-byte chunks of fp16, or of
+                           // fp32 for an fp16 output, [2 n_ctas][chunk][tile]
   float* part_lse;         // [2 n_ctas][rows of a tile], base 2
 };
 

@@ -235,8 +235,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
             }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->raw_empty[slot]);   // (the block is in registers)
         // a page that is not there: code 0 at scale 0 for all
         if (!there) {
           ks = vs[0] = vs[1] = 0;
@@ -316,7 +314,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->kv_full[b]);
+          if (lane == 0) {
+            mbar_arrive(&bars->kv_full[b]);
+            // The block's slot is free only now that all its values have been used: an arrival behind the loads alone let the
+            // next copy meet loads of V that were still under way
+            mbar_arrive(&bars->raw_empty[slot]);
+          }
           ++item;
         }
       }

@@ -665,3 +665,33 @@ def test_captured_attention_is_repeatable_beside_another_stream(T):
         torch.cuda.synchronize()
         assert torch.equal(out, first) and torch.equal(out2, want2)
     assert dg.dg_kv4_error(c) == 0 and dg.dg_kv4_error(other) == 0
+
+
+@pytest.mark.parametrize("T,dh,lens", [(256, 128, [4000]), (256, 128, [3000, 700, 2900, 3000, 64, 2000, 1500, 3000]), (256, 64, [3000]),
+                                       (64, 64, [700, 650]), (1, 128, [4000]), (1, 128, [32000]), (4, 128, [3000] * 8)])
+def test_attention_is_repeatable_under_load(T, dh, lens):
+    """A call gives the same bits beside calls that fill the memory system: its copies of pages come late and close together then,
+    and must not meet values that are still being read."""
+    c, busy = make(8, dh, lens), make(8, 128, [6000] * 8, seed=9)
+    q = torch.randn((len(lens), T, 16, dh), device="cuda").to(BF16)
+    out, lse = torch.empty_like(q), torch.empty((len(lens), T, 16), device="cuda")
+    loads = []
+    for rows in (256, 1):
+        x = torch.randn((8, rows, 16, 128), device="cuda").to(BF16)
+        loads.append((x, torch.empty_like(x),
+                      torch.empty(dg.dg_kv4_attend_workspace_bytes(busy, 16, rows), dtype=torch.uint8, device="cuda")))
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 16, T), dtype=torch.uint8, device="cuda")
+    dg.dg_kv4_attend(c, 0, q, out, ws, lse=lse)
+    torch.cuda.synchronize()
+    want, want_lse = out.clone(), lse.clone()
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(400):
+        with torch.cuda.stream(s):
+            dg.dg_kv4_attend(busy, 0, *loads[i % 2])
+        with torch.cuda.stream(s2):
+            out.zero_()
+            dg.dg_kv4_attend(c, 0, q, out, ws, lse=lse)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse), i
+    assert dg.dg_kv4_error(c) == 0 and dg.dg_kv4_error(busy) == 0

@@ -13,7 +13,8 @@ namespace dg {
 namespace {
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
+  // (volatile: no product, and so no load that it waits for, falls behind the copy that refills a slot)
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -47,9 +48,9 @@ struct FewSmem {
   float m[kFewWarps][kKv4FewTile], l[kFewWarps][kKv4FewTile];
 };
 
-// Cluster: grid (unit, 1, CTA of the unit's cluster); else the CTAs divide the line.
+// Cluster: grid (tile, KV head, CTA of the cluster for each sequence); else the CTAs divide the line.
 template <int DH, typename T, bool Cluster>
-__global__ void __launch_bounds__(32 * kFewWarps)
+__global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
     kv4_attend_few_kernel(Kv4View c, int layer, Kv4Attn a) {
   using F = Kv4<DH>;
   constexpr int NJ = DH / 16;            // 16-channel steps of a row
@@ -65,6 +66,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
   pdl_wait();
 
   const int G = a.group;
+  const Unit unit = Cluster ? cluster_unit() : Unit{0, 0, 0, 0, 1};
   int phase = 0;                // copies that each stage of the ring has seen, one bit each: its barrier's parity
   bool ok = true;
   // one piece of work
@@ -73,8 +75,8 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     const SeqView sv = pc.v;
     const int r0 = pc.tile * kKv4FewTile;         // row r of the group: query row r / G, head r % G of the group
     const int nr = min(kKv4FewTile, sv.n * G - r0);
-    const int limit = row_limit(sv, (r0 + nr - 1) / G, a.causal);   // the tile's last row sees the most
-    const int all = row_limit(sv, r0 / G, a.causal);                // every row sees positions below this
+    const int limit = row_limit(sv, group_row(a, r0 + nr - 1), a.causal);   // the tile's last row sees the most
+    const int all = row_limit(sv, group_row(a, r0), a.causal);                // every row sees positions below this
     const int p0 = pc.s0, p1 = min((limit + kPage - 1) / kPage, pc.s1);
     const int n_mine = p1 - p0 > warp ? (p1 - p0 - warp + kFewWarps - 1) / kFewWarps : 0;
 
@@ -115,12 +117,12 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     uint32_t qf[NJ][2];
     float fac[2];                 // rows 2t, 2t + 1: scale log2(e) and the power of two taken out
     {
-      const int r = r0 + g;
+      const int r = r0 + g, qj = group_row(a, r);
       float x[DH / 4];
 #pragma unroll
       for (int i = 0; i < DH / 4; ++i) x[i] = 0.f;
       if (g < nr) {
-        const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + (r / G) * a.q_row + (head * G + r % G) * a.q_head +
+        const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + qj * a.q_row + (head * G + r - qj * G) * a.q_head +
                      DH / 4 * t;
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     }
     int lim[2];                   // positions that rows 2t, 2t + 1 see
 #pragma unroll
-    for (int e = 0; e < 2; ++e) lim[e] = 2 * t + e < nr ? row_limit(sv, (r0 + 2 * t + e) / G, a.causal) : 0;
+    for (int e = 0; e < 2; ++e) lim[e] = 2 * t + e < nr ? row_limit(sv, group_row(a, r0 + 2 * t + e), a.causal) : 0;
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float o[NJ][4];               // O^T: channels DH/8 g + 2 j + {0, 1}, rows 2t, 2t + 1
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         v1 /= den;
       }
       const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(den);
-      const int r = r0 + row, j = r / G, h = head * G + r % G;
-      if (Cluster && gridDim.z > 1) {
+      const int r = r0 + row, j = group_row(a, r), h = head * G + r - j * G;
+      if (Cluster && unit.n > 1) {
         *reinterpret_cast<float2*>(part + row * DH + ch) = make_float2(v0, v1);
         if (ch == 0) part_lse[row] = lse2;
       } else if (pc.whole()) {
@@ -345,12 +347,12 @@ __global__ void __launch_bounds__(32 * kFewWarps)
         if (ch == 0) a.part_lse[at] = lse2;
       }
     }
-    if (Cluster && gridDim.z > 1) {
+    if (Cluster && unit.n > 1) {
       // every CTA of the cluster joins its share of the rows' channel pairs from all of them
       cluster_sync();
-      const int n = gridDim.z;
+      const int n = unit.n;
       const uint32_t o_addr = smem_u32(part), lse_addr = smem_u32(part_lse);
-      for (int i = blockIdx.z * 32 * kFewWarps + threadIdx.x; i < nr * (DH / 2); i += n * 32 * kFewWarps) {
+      for (int i = unit.rank * 32 * kFewWarps + threadIdx.x; i < nr * (DH / 2); i += n * 32 * kFewWarps) {
         const int row = i / (DH / 2), ch = i % (DH / 2) * 2;
         float le[kMaxCluster];
         float2 x[kMaxCluster];
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(32 * kFewWarps)
           v0 /= den;
           v1 /= den;
         }
-        const int r = r0 + row, j = r / G, h = head * G + r % G;
+        const int r = r0 + row, j = group_row(a, r), h = head * G + r - j * G;
         T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + ch;
         *reinterpret_cast<uint32_t*>(dst) = Half<T>::pack(v0, v1);
         if (a.lse && ch == 0)
@@ -385,19 +387,17 @@ __global__ void __launch_bounds__(32 * kFewWarps)
     }
   };
   if constexpr (Cluster) {
-    // unit: (sequence, KV head, tile) with the tiles that `rows` rows would have
-    const int tiles = (a.rows * G + kKv4FewTile - 1) / kKv4FewTile;
     Piece pc;
-    pc.tile = blockIdx.x % tiles;
-    pc.head = blockIdx.x / tiles % c.n_kv;
-    pc.seq = blockIdx.x / tiles / c.n_kv;
+    pc.tile = unit.tile;
+    pc.head = unit.head;
+    pc.seq = unit.seq;
     pc.v = seq_view(c, a, pc.seq, threadIdx.x == 0);
     if (pc.tile * kKv4FewTile >= pc.v.n * G) return;   // (the whole cluster)
     const int pages = (pc.v.len + kPage - 1) / kPage;
-    const int per = (pages + gridDim.z - 1) / gridDim.z;
+    const int per = (pages + unit.n - 1) / unit.n;
     pc.cost = max(1, pages);
-    pc.s0 = gridDim.z == 1 ? 0 : min(pages, (int)blockIdx.z * per);
-    pc.s1 = gridDim.z == 1 ? pc.cost : min(pages, pc.s0 + per);
+    pc.s0 = unit.n == 1 ? 0 : min(pages, unit.rank * per);
+    pc.s1 = unit.n == 1 ? pc.cost : min(pages, pc.s0 + per);
     pc.first = true;
     work(pc);
   } else {
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
     }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
-  const int j = r / G, h = head * G + r % G;
+  const int j = group_row(a, r), h = head * G + r - j * G;
   uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * 8);
 #pragma unroll
   for (int u = 0; u < 2; ++u)
@@ -592,8 +592,8 @@ cudaError_t launch_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream
   });
   if (e != cudaSuccess) return e;
   if (a.cluster) {
-    const int units = (a.rows * a.group + kKv4FewTile - 1) / kKv4FewTile * c.n_kv * c.n_seq;
-    return launch_k(kv4_attend_few_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(32 * kFewWarps),
+    const int tiles = (a.rows * a.group + kKv4FewTile - 1) / kKv4FewTile;
+    return launch_k(kv4_attend_few_kernel<DH, T, true>, dim3(tiles, c.n_kv, c.n_seq * a.cluster), dim3(32 * kFewWarps),
                     sizeof(FewSmem<DH>), st, a.cluster, c, layer, a);
   }
   return launch_k(kv4_attend_few_kernel<DH, T, false>, dim3(a.n_ctas), dim3(32 * kFewWarps),

@@ -50,6 +50,25 @@ __device__ __forceinline__ SeqView seq_view(const Kv4View& c, const Kv4Attn& a, 
   return v;
 }
 
+// query row of row r of the group (r / group by a multiplication: r < 2^31; a division by a variable costs 150 cycles)
+__device__ __forceinline__ int group_row(const Kv4Attn& a, int r) {
+  return (int)((__umulhi((uint32_t)r, a.group_mul) + (uint32_t)r) >> a.group_shift);
+}
+
+// The unit of a cluster, from the grid (tile, KV head, CTAs of the cluster for each sequence); this CTA's rank of n.
+struct Unit {
+  int tile, head, seq, rank, n;
+};
+__device__ __forceinline__ Unit cluster_unit() {
+  Unit u;
+  u.tile = blockIdx.x;
+  u.head = blockIdx.y;
+  asm("mov.u32 %0, %%clusterid.z;" : "=r"(u.seq));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(u.rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(u.n));
+  return u;
+}
+
 // positions that row j of n sees
 __device__ __forceinline__ int row_limit(const SeqView& v, int j, int causal) {
   return causal ? max(0, min(v.len, v.len - v.n + j + 1)) : v.len;
@@ -193,6 +212,17 @@ __device__ __forceinline__ float dsmem_ld_f1(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void dsmem_st_f1(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void dsmem_st4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Channels in a 16-byte chunk of a part of the many-rows form: fp16 for a bf16 output, fp32 for an fp16 one.
 template <typename T>

@@ -16,8 +16,11 @@
 // P as the tensor core's operand in TMEM and not in shared memory takes 128 KB off the 384 KB that 128 positions
 // cost there; the blocks come by bulk copies because loads into registers were waited for by each tile's proxy fence.
 //
-// A call whose units fit the SMs in clusters runs one for each unit: its CTAs leave their rows in shared memory, where
-// each joins a share of them through distributed shared memory, and the second launch falls away.
+// A call whose units fit the SMs in clusters runs one for each unit, whose CTAs each join a share of its rows, and the second
+// launch falls away.  A row goes from TMEM into its place in the Q tile and from there in one piece into the shared memory of the CTA that
+// joins it.  Such a call is a chain of latencies (one canvas behind 2048 positions: 19.1 us, 6 of them its six steps), so Q
+// is copied asynchronously while the lengths are read, a thread scales a row of it from registers (1.5 us less than
+// sixteen rounds of loads, shuffles and stores), and no index is divided by a variable.
 //
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
 // positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in the same
@@ -45,9 +48,10 @@ template <int DH>
 struct ManySmem {
   static constexpr uint32_t kQ = 128u * DH * 2u;       // a Q tile
   static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
-  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024;
+  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024 + 4 * kMaxManyCluster;
   static_assert(kBytes <= 232448, "shared memory budget");
-  static_assert(kRing * kTile == 256u * DH * 4u, "the ring holds a CTA's rows in fp32");
+  static_assert(kRing * kTile + kRaw * Kv4<DH>::kBytes >= (256u + kMaxManyCluster - 1) * DH * 4u,
+                "the rings hold the rows in fp32 that a cluster's CTA joins: of n CTAs, each at most 1/n of 256, rounded up");
 };
 
 // A piece of work as the roles need it.
@@ -141,7 +145,7 @@ struct Tasks {
   }
 };
 
-// Cluster: grid (unit, 1, CTA of the unit's cluster); else the CTAs divide the line.
+// Cluster: grid (tile, KV head, CTA of the cluster for each sequence); else the CTAs divide the line.
 template <int DH, typename T, bool Cluster>
 __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4View c, int layer, Kv4Attn a) {
   using F = Kv4<DH>;
@@ -188,6 +192,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   pdl_wait();
 
   const int G = a.group;
+  const Unit unit = Cluster ? cluster_unit() : Unit{0, 0, 0, 0, 1};
   Tasks tasks{bars, err};
   Task pc;
   bool ok = true;
@@ -324,29 +329,33 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         }
       }
     }
-    if constexpr (Cluster) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    if constexpr (Cluster) {
+      __syncwarp();
+      if (unit.n > 1) cluster_sync();
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 13) {
       // ------------------------------ pieces ------------------------------
       auto task_of = [&](const Piece& p) {
         const int row0 = p.tile * kKv4ManyTile, nr = min(kKv4ManyTile, p.v.n * G - row0);
-        const int limit = row_limit(p.v, (row0 + nr - 1) / G, a.causal);   // the last row sees the most
+        const int limit = row_limit(p.v, group_row(a, row0 + nr - 1), a.causal);   // the last row sees the most
         const int steps = max(0, min((limit + kKv4ManyStep - 1) / kKv4ManyStep, p.s1) - p.s0);
         return Task{p.seq, p.head, row0, nr, p.s0, steps, p.v.len, p.v.n, p.whole(), (int)slot_of(p)};
       };
       const Task none{0, 0, 0, 0, 0, -1, 0, 0, 0, 0};
       if constexpr (Cluster) {
         // one piece: this CTA's share of the unit's pages; the unit may have no rows
-        const int tiles = (a.rows * G + kKv4ManyTile - 1) / kKv4ManyTile, n = gridDim.z;
+        const int n = unit.n;
         Piece p;
-        p.tile = blockIdx.x % tiles;
-        p.head = blockIdx.x / tiles % c.n_kv;
-        p.seq = blockIdx.x / tiles / c.n_kv;
+        p.tile = unit.tile;
+        p.head = unit.head;
+        p.seq = unit.seq;
         p.v = seq_view(c, a, p.seq, lane == 0);
         const int pages = (p.v.len + kPage - 1) / kPage, per = (pages + n - 1) / n;
         p.cost = max(1, pages);
-        p.s0 = n == 1 ? 0 : min(pages, (int)blockIdx.z * per);
+        p.s0 = n == 1 ? 0 : min(pages, unit.rank * per);
         p.s1 = n == 1 ? p.cost : min(pages, p.s0 + per);
         p.first = true;
         if (lane == 0) {
@@ -476,7 +485,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       }
     }
     __syncwarp();
-    if constexpr (Cluster) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    if constexpr (Cluster) {
+      if (unit.n > 1) cluster_sync();
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ------------------------------ softmax ------------------------------
@@ -484,6 +496,32 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lane_off + 256 + x * 128;
     uint8_t* qtile = q_s + x * C::kQ + (warp & 3) * 32 * 128;   // this warp's 32 rows
+    auto q_chunk = [&](int row, int i) {         // 16-byte chunk i of the warp's row
+      return reinterpret_cast<uint4*>(qtile + (i / 8) * 16384 + row * 128 + (((i & 7) ^ (row & 7)) << 4));
+    };
+    // The warp's rows of Q as they are into their places, dh / 8 lanes a row.  (All rows that the tensor has: those behind
+    // the sequence's last one are set to zero when they are scaled.)
+    auto load_q = [&](int seq, int head, int row0) {
+      constexpr int kLanes = DH / 8, kRows = 32 / kLanes;
+      const int first = x * 128 + (warp & 3) * 32 + lane / kLanes;   // row of round 0, then kRows further each
+      int qj = group_row(a, row0 + first), qg = row0 + first - qj * G;
+      const int dj = group_row(a, kRows), dg = kRows - dj * G;
+      const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + (head * G) * a.q_head + lane % kLanes * 8;
+#pragma unroll 4
+      for (int i = 0; i < 32 / kRows; ++i) {
+        if (qj < a.rows) cp_async16(q_chunk(i * kRows + lane / kLanes, lane % kLanes), q + qj * a.q_row + qg * a.q_head);
+        qj += dj;
+        qg += dg;
+        if (qg >= G) {
+          qg -= G;
+          ++qj;
+        }
+      }
+    };
+    bool met = false;                            // the cluster, before its rows are written
+    if constexpr (Cluster) {
+      load_q(unit.seq, unit.head, unit.tile * kKv4ManyTile);   // (while the lengths are on their way)
+    }
     uint32_t n_step = 0;                         // steps of this tile so far
     while (tasks.next(pc)) {
       const int steps = pc.steps;
@@ -491,64 +529,37 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const bool valid = x * 128 + r < pc.nr;
       // a row behind the last one goes along with its limit, so that its warp's shortcuts hold
       const int rr = pc.row0 + (valid ? x * 128 + r : pc.nr - 1);
-      const int j = rr / G, h = pc.head * G + rr % G;
+      const int j = group_row(a, rr), h = pc.head * G + rr - j * G;
       const int limit = row_limit(SeqView{pc.len, pc.n}, j, a.causal);
       float sl2 = 0.f;
       if (steps > 0) {
-        // Q to fp16 in the swizzled layout, times a power of two: dh / 8 lanes a row, so that a row is read in one
-        // piece (the S products of the last piece, which read these rows, are complete: this warp has read the last S)
-        constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kN = 32 / kRows;   // kN rounds of kRows rows; kN == kLanes
-        const int sub = lane % kLanes;
-        uint4 all[kN];
-        {
-          const int first = x * 128 + (warp & 3) * 32 + lane / kLanes;   // row of round 0, then kRows further each
-          int qj = (pc.row0 + first) / G, qg = (pc.row0 + first) % G;
-          const int dj = kRows / G, dg = kRows % G;
-          const T* q = static_cast<const T*>(a.q) + pc.seq * a.q_seq + (pc.head * G) * a.q_head + sub * 8;
+        // Q to fp16 in its place, times a power of two, a thread a row.  (The S products of the last piece, which read these
+        // rows, are complete: this warp has read the last S)
+        if constexpr (!Cluster) load_q(pc.seq, pc.head, pc.row0);
+        cp_async_wait_all();
+        __syncwarp();
+        uint4 w[DH / 8];
+        uint32_t top[4] = {0, 0, 0, 0};   // largest magnitudes: 16-bit floats in the order of their bits
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            all[i] = make_uint4(0, 0, 0, 0);
-            if (first + i * kRows < pc.nr) all[i] = *reinterpret_cast<const uint4*>(q + qj * a.q_row + qg * a.q_head);
-            qj += dj;
-            qg += dg;
-            if (qg >= G) {
-              qg -= G;
-              ++qj;
-            }
-          }
+        for (int i = 0; i < DH / 8; ++i) w[i] = *q_chunk(lane, i);   // (all before the first store)
+#pragma unroll
+        for (int i = 0; i < DH / 8; ++i) {
+          if (!valid) w[i] = make_uint4(0, 0, 0, 0);
+          top[0] = __vmaxu2(top[0], w[i].x & 0x7fff7fffu);
+          top[1] = __vmaxu2(top[1], w[i].y & 0x7fff7fffu);
+          top[2] = __vmaxu2(top[2], w[i].z & 0x7fff7fffu);
+          top[3] = __vmaxu2(top[3], w[i].w & 0x7fff7fffu);
         }
-        // largest magnitudes: kN values a lane, reduced over the kLanes lanes of a row so that lane k ends with round k's
-        float mx[kN];
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const uint32_t wd[4] = {all[i].x, all[i].y, all[i].z, all[i].w};
-          mx[i] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[i] = max3(mx[i], fabsf(Half<T>::lo(wd[e])), fabsf(Half<T>::hi(wd[e])));
-        }
-#pragma unroll
-        for (int o = kN / 2; o >= 1; o /= 2) {
-          const bool upper = sub & o;
-#pragma unroll
-          for (int k = 0; k < o; ++k) {
-            const float other = __shfl_xor_sync(0xffffffffu, upper ? mx[k] : mx[k + o], o);
-            mx[k] = fmaxf(upper ? mx[k + o] : mx[k], other);
-          }
-        }
+        top[0] = __vmaxu2(__vmaxu2(top[0], top[1]), __vmaxu2(top[2], top[3]));
         float down, up;
-        row_powers(mx[0], down, up);
+        row_powers(Half<T>::lo(max(top[0] & 0xffffu, top[0] >> 16)), down, up);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int row = i * kRows + lane / kLanes;
-          const float d = __shfl_sync(0xffffffffu, down, lane - sub + i);
-          uint32_t wd[4] = {all[i].x, all[i].y, all[i].z, all[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) wd[e] = pack_f16x2(Half<T>::lo(wd[e]) * d, Half<T>::hi(wd[e]) * d);
-          *reinterpret_cast<uint4*>(qtile + (sub / 8) * 16384 + row * 128 + (((sub & 7) ^ (row & 7)) << 4)) =
-              make_uint4(wd[0], wd[1], wd[2], wd[3]);
-        }
-        const float mine = __shfl_sync(0xffffffffu, up, (lane % kRows) * kLanes + lane / kRows);   // of row `lane`
-        sl2 = fmaxf(a.scale * 1.4426950408889634f * mine, 1e-44f);   // (above 0, so that -inf stays -inf)
+        for (int i = 0; i < DH / 8; ++i)
+          *q_chunk(lane, i) = make_uint4(pack_f16x2(Half<T>::lo(w[i].x) * down, Half<T>::hi(w[i].x) * down),
+                                         pack_f16x2(Half<T>::lo(w[i].y) * down, Half<T>::hi(w[i].y) * down),
+                                         pack_f16x2(Half<T>::lo(w[i].z) * down, Half<T>::hi(w[i].z) * down),
+                                         pack_f16x2(Half<T>::lo(w[i].w) * down, Half<T>::hi(w[i].w) * down));
+        sl2 = fmaxf(a.scale * 1.4426950408889634f * up, 1e-44f);   // (above 0, so that -inf stays -inf)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_full[x]);
@@ -640,104 +651,127 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
                             pack_f16x2(o[e + 4], o[e + 5]), pack_f16x2(o[e + 6], o[e + 7]));
       };
       uint4* part = static_cast<uint4*>(a.part_o) + (size_t)pc.slot * kKv4ManyTile * (DH / kPer) + x * 128 + r;
-      if (Cluster && gridDim.z > 1) {
-        // the tiles' buffers become the CTA's rows once both tiles' products are complete
-        asm volatile("bar.sync 1, %0;" ::"r"(pc.nr > 128 ? 256 : 128) : "memory");
-      }
+      if (Cluster && unit.n > 1) {
+        // Each CTA of the cluster joins its share of the rows.  A row goes into this warp's part of the Q tile, whose products
+        // are complete, and from there in one piece to the CTA that joins it: as the lanes hold the rows, a store would
+        // meet a line for each lane
+        const int per = (pc.nr + unit.n - 1) / unit.n, owner = min((x * 128 + r) / per, unit.n - 1);
+        const int place = unit.rank * per + x * 128 + r - owner * per;
+        const uint32_t to = dsmem_map(smem_u32(kv_s) + place * (16 * DH / kPer), owner);
+        const uint32_t to_lse = dsmem_map(smem_u32(lse_s) + 4 * place, owner);
+        cluster_sync();   // the others' rings are free once all their products are complete
+        met = true;
+        if (valid) dsmem_st_f1(to_lse, lse2);
+        constexpr int kLanes = DH / 8, kRows = 32 / kLanes;   // the Q tile holds dh / 8 chunks of a row
 #pragma unroll
-      for (int cb = 0; cb < DH; cb += 32) {
-        float o[32];
-        tmem_ld32(t_o + cb, o);
-        tmem_wait_ld();
+        for (int half = 0; half < 8 / kPer; ++half) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
-        if (Cluster && gridDim.z > 1) {
-          // row r's 16-byte chunks, swizzled for the banks
+          for (int cb = 0; cb < DH / 8 * kPer; cb += 32) {
+            float o[32];
+            tmem_ld32(t_o + half * (DH / 2) + cb, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += kPer)
-            *reinterpret_cast<uint4*>(kv_s + (x * 128 + r) * (16 * DH / kPer) +
-                                      ((((cb + e) / kPer) ^ (r & 7)) << 4)) = chunk_of(o, e);
-        } else if (valid && ok) {
-          if (pc.whole) {
+            for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + cb + e) =
-                  make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
-                             Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
-          } else {
+            for (int e = 0; e < 32; e += kPer) *q_chunk(lane, (cb + e) / kPer) = chunk_of(o, e);
+          }
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; e += kPer) part[(cb + e) / kPer * kKv4ManyTile] = chunk_of(o, e);
+          for (int i = 0; i < 32 / kRows; ++i) {
+            const int row = i * kRows + lane / kLanes;
+            const uint32_t at = __shfl_sync(0xffffffffu, to, row) + (half * kLanes + lane % kLanes) * 16;
+            if (x * 128 + (warp & 3) * 32 + row < pc.nr) dsmem_st4(at, *q_chunk(row, lane % kLanes));
+          }
+          __syncwarp();
+        }
+      } else {
+#pragma unroll
+        for (int cb = 0; cb < DH; cb += 32) {
+          float o[32];
+          tmem_ld32(t_o + cb, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
+          if (valid && ok) {
+            if (pc.whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(dst + cb + e) =
+                    make_uint4(Half<T>::pack(o[e], o[e + 1]), Half<T>::pack(o[e + 2], o[e + 3]),
+                               Half<T>::pack(o[e + 4], o[e + 5]), Half<T>::pack(o[e + 6], o[e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += kPer) part[(cb + e) / kPer * kKv4ManyTile] = chunk_of(o, e);
+            }
           }
         }
-      }
-      if (Cluster && gridDim.z > 1) {
-        lse_s[x * 128 + r] = lse2;
-      } else if (valid && ok) {
-        if (!pc.whole)
-          a.part_lse[at] = lse2;
-        else if (a.lse)
-          a.lse[((size_t)pc.seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
+        if (valid && ok) {
+          if (!pc.whole)
+            a.part_lse[at] = lse2;
+          else if (a.lse)
+            a.lse[((size_t)pc.seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
+        }
       }
       tc_fence_before();   // O is read before the next piece's products overwrite it (they wait for p_ready)
     }
     // (a cluster's CTA goes on with all its warps: everyone back to the registers of the launch)
-    if constexpr (Cluster) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    if constexpr (Cluster) {
+      cp_async_wait_all();
+      __syncwarp();
+      if (unit.n > 1 && !met) cluster_sync();
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 12) tmem_dealloc(tmem, 512);
-  if (Cluster && gridDim.z > 1) {
-    // every CTA of the cluster joins its share of the unit's rows, a thread for a 16-byte chunk at a time
+  if (Cluster && unit.n > 1) {
+    // every CTA of the cluster has its share of the unit's rows from all of them, and joins it, a thread for a 16-byte chunk at a time
     cluster_sync();
-    const int tiles = (a.rows * G + kKv4ManyTile - 1) / kKv4ManyTile, n = gridDim.z;
-    const int tile = blockIdx.x % tiles, head = blockIdx.x / tiles % c.n_kv, seq = blockIdx.x / tiles / c.n_kv;
-    const int nr = min(kKv4ManyTile, seq_view(c, a, seq).n * G - tile * kKv4ManyTile);
-    const int per = (nr + n - 1) / n;   // rows of a CTA (nr <= 0: none)
+    const int n = unit.n, nr = bars->task[0].nr;                 // (0: the unit has no rows)
+    const int per = (nr + n - 1) / n, first = unit.rank * per, mine = min(per, nr - first);
     constexpr int kPer = kPartPer<T>, kChunks = DH / kPer;
-    const uint32_t o_addr = smem_u32(kv_s), lse_addr = smem_u32(lse_s);
-    for (int i = threadIdx.x; i < per * kChunks; i += kManyThreads) {
-      const int at = blockIdx.z * per + i / kChunks, chunk = i % kChunks;
-      if (at >= nr) break;
-      const uint32_t off = o_addr + (at * kChunks + (chunk ^ (at & 7))) * 16;
+    for (int i = threadIdx.x; i < mine * kChunks; i += kManyThreads) {
+      const int at = i / kChunks, chunk = i % kChunks;
       float le[kMaxManyCluster], top = -INFINITY;
-      float4 x[kMaxManyCluster];
+      uint4 v[kMaxManyCluster];
 #pragma unroll
-      for (int k = 0; k < kMaxManyCluster; ++k) {
-        le[k] = k < n ? dsmem_ld_f1(dsmem_map(lse_addr + 4 * at, k)) : -INFINITY;
-        x[k] = k < n ? dsmem_ld_f4(dsmem_map(off, k)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        top = max_nan(top, le[k]);
+      for (int k = 0; k < kMaxManyCluster; ++k) {   // (all loads before the first use)
+        le[k] = k < n ? lse_s[k * per + at] : -INFINITY;
+        v[k] = k < n ? reinterpret_cast<const uint4*>(kv_s)[(k * per + at) * kChunks + chunk] : make_uint4(0, 0, 0, 0);
       }
+#pragma unroll
+      for (int k = 0; k < kMaxManyCluster; ++k) top = max_nan(top, le[k]);
       float acc[kPer], den = 0.f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
       if (top != -INFINITY) {
 #pragma unroll
         for (int k = 0; k < kMaxManyCluster; ++k) {
-          const float f = k < n ? fast_exp2(le[k] - top) : 0.f;
-          const float w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          const float f = fast_exp2(le[k] - top);
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           den += f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (kPer == 4) {
-              acc[e] += f * w[e];
+              acc[e] += f * __uint_as_float(w[e]);
             } else {
-              acc[2 * e] += f * Half<__half>::lo(__float_as_uint(w[e]));
-              acc[2 * e + 1] += f * Half<__half>::hi(__float_as_uint(w[e]));
+              acc[2 * e] += f * Half<__half>::lo(w[e]);
+              acc[2 * e + 1] += f * Half<__half>::hi(w[e]);
             }
           }
         }
       }
       const float inv = den == 0.f ? 0.f : 1.f / den;
-      const int rr = tile * kKv4ManyTile + at, j = rr / G, h = head * G + rr % G;
-      T* dst = static_cast<T*>(a.out) + seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * kPer;
+      const int rr = unit.tile * kKv4ManyTile + first + at, j = group_row(a, rr), h = unit.head * G + rr - j * G;
+      T* dst = static_cast<T*>(a.out) + unit.seq * a.o_seq + j * a.o_row + h * a.o_head + chunk * kPer;
 #pragma unroll
       for (int e = 0; e < kPer; e += 4)
         *reinterpret_cast<uint2*>(dst + e) = make_uint2(Half<T>::pack(acc[e] * inv, acc[e + 1] * inv),
                                                         Half<T>::pack(acc[e + 2] * inv, acc[e + 3] * inv));
       if (a.lse && chunk == 0)
-        a.lse[((size_t)seq * a.rows + j) * a.n_q + h] = (top + log2f(den)) * 0.6931471805599453f;
+        a.lse[((size_t)unit.seq * a.rows + j) * a.n_q + h] = (top + log2f(den)) * 0.6931471805599453f;
     }
-    cluster_sync();   // this CTA's rows stay until all have read them
   }
 }
 
@@ -780,8 +814,8 @@ cudaError_t launch_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStrea
   const cudaError_t e = prepare_many<DH, T>();
   if (e != cudaSuccess) return e;
   if (a.cluster) {
-    const int units = (a.rows * a.group + kKv4ManyTile - 1) / kKv4ManyTile * c.n_kv * c.n_seq;
-    return launch_k(kv4_attend_many_kernel<DH, T, true>, dim3(units, 1, a.cluster), dim3(kManyThreads), kBytes, st,
+    const int tiles = (a.rows * a.group + kKv4ManyTile - 1) / kKv4ManyTile;
+    return launch_k(kv4_attend_many_kernel<DH, T, true>, dim3(tiles, c.n_kv, c.n_seq * a.cluster), dim3(kManyThreads), kBytes, st,
                     a.cluster, c, layer, a);
   }
   return launch_k(kv4_attend_many_kernel<DH, T, false>, dim3(a.n_ctas), dim3(kManyThreads), kBytes, st, 1, c, layer, a);

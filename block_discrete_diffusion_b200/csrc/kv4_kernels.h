@@ -49,6 +49,8 @@ struct Kv4Attn {
   long long q_seq, q_row, q_head, o_seq, o_row, o_head;
   int n_q, rows, causal, fp16;
   int group;               // query heads of a KV head
+  uint32_t group_mul;      // r / group = (high word of r * group_mul, plus r) >> group_shift
+  int group_shift;
   float scale;
   int cluster;             // CTAs of a unit's cluster (the rows are joined there), 0: divide the line
   int n_ctas;              // CTAs among which the work is divided
@@ -62,6 +64,8 @@ struct Kv4Attn {
 // Few rows of a KV head (single tokens): tiles of 8 rows, steps of one page, mma.sync on fragments dequantised in
 // registers.  Many rows (canvases, prompt chunks): tiles of 256 rows, steps of one page, tcgen05.
 constexpr int kKv4FewTile = 8, kKv4FewStep = 64, kKv4MaxCluster = 16;
+// CTAs of the few-rows form that an SM holds at once: by shared memory, by registers.
+constexpr __host__ __device__ int kv4_few_ctas(int dh) { return dh == 128 ? 3 : 4; }
 constexpr int kKv4ManyTile = 256, kKv4ManyStep = 64, kKv4MaxManyCluster = 8;
 cudaError_t kv4_attend_few(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);
 cudaError_t kv4_attend_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStream_t st);

@@ -638,6 +638,26 @@ def test_output_over_the_queries(T, table):
     assert torch.equal(out, q)
 
 
+@pytest.mark.parametrize("T,n_q,n_kv,dh", [(256, 16, 8, 128), (256, 10, 2, 64), (130, 7, 1, 128), (7, 16, 8, 128), (12, 15, 3, 64)])
+@pytest.mark.parametrize("table", [None, 3000])
+def test_queries_behind_the_last_row_do_not_matter(T, n_q, n_kv, dh, table):
+    """Whatever the queries behind a sequence's last row hold, the rows before them are the same and theirs are left alone."""
+    c, rows = make(n_kv, dh, [700, 300], max_pages=table), [T - 3, 2]
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, n_q, T), dtype=torch.uint8, device="cuda")
+    q = torch.randn((2, T, n_q, dh), device="cuda").to(BF16)
+    outs = []
+    for x in (0.0, float("nan"), float("inf")):
+        for s, n in enumerate(rows):
+            q[s, n:] = x
+        out = torch.full_like(q, 7.0)
+        dg.dg_kv4_attend(c, 0, q, out, ws, rows=dev(rows))
+        outs.append(out)
+    for s, n in enumerate(rows):
+        assert bool((outs[0][s, n:] == 7).all()) and bool(outs[0][s, :n].isfinite().all())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert dg.dg_kv4_error(c) == 0
+
+
 @pytest.mark.parametrize("T", [1, 64, 256])
 def test_captured_attention_is_repeatable_beside_another_stream(T):
     """Replays of a captured call give the same bits while another cache's calls run on another stream."""

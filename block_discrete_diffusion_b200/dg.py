@@ -365,6 +365,7 @@ class Kv4Cache:
         self.c, self.pool, self.book = c, pool, book
         self.ref = ctypes.byref(c)
         self.device, self.index = pool.device, pool.device.index
+        self.n_seq, self.n_kv, self.d_head = c.n_seq, c.n_kv, c.d_head   # (a read of the C struct takes longer)
         pad = lambda n: (n + 3) // 4 * 4   # noqa: E731
         refs = 16 + pad(c.n_seq)
         table = refs + pad(c.n_pages)
@@ -450,7 +451,7 @@ def dg_kv4_init(cache: Kv4Cache, stream=None):
 
 def dg_kv4_extend(cache: Kv4Cache, counts, stream=None):
     """counts int32 [n_seq]: positions by which each sequence grows."""
-    _check("dg_kv4_extend", lib().dg_kv4_extend(cache.ref, _kv4_ints(cache, counts, cache.c.n_seq, "counts"),
+    _check("dg_kv4_extend", lib().dg_kv4_extend(cache.ref, _kv4_ints(cache, counts, cache.n_seq, "counts"),
                                                 _kv4_stream(cache, stream)))
 
 
@@ -471,12 +472,11 @@ def dg_kv4_compact(cache: Kv4Cache, stream=None):
 
 
 def _kv4_rows(fn, cache, layer, k, v, rows, stream):
-    c = cache.c
-    shape = (c.n_seq, k.shape[1] if k.dim() == 4 else -1, c.n_kv, c.d_head)
+    shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d_head)
     code, ks = _kv4_tensor(cache, k, shape, "k")
     _, vs = _kv4_tensor(cache, v, shape, "v", k.dtype)
     r = dg_kv4_rows(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                    _kv4_ints(cache, rows, c.n_seq, "rows"), shape[1], code)
+                    _kv4_ints(cache, rows, cache.n_seq, "rows"), shape[1], code)
     _check(fn, getattr(lib(), fn)(cache.ref, layer, ctypes.byref(r), _kv4_stream(cache, stream)))
 
 
@@ -499,22 +499,21 @@ def dg_kv4_attend_workspace_bytes(cache: Kv4Cache, n_q, rows) -> int:
 def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale=None, causal=False, stream=None):
     """q, out [n_seq, T, n_q, d_head] (any strides with contiguous channels), lse fp32 [n_seq, T, n_q]; scale defaults to
     d_head^-0.5; rows as in dg_kv4_append."""
-    c = cache.c
-    if q.dim() != 4:
-        raise ValueError("q: expected [n_seq, T, n_q, d_head]")
-    shape = (c.n_seq, q.shape[1], q.shape[2], c.d_head)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != cache.n_seq or shape[3] != cache.d_head:
+        raise ValueError(f"q: expected [{cache.n_seq}, T, n_q, {cache.d_head}], got {tuple(shape)}")
     code, qs = _kv4_tensor(cache, q, shape, "q")
     _, os_ = _kv4_tensor(cache, out, shape, "out", q.dtype)
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()
                             or lse.get_device() != cache.index):
-        raise ValueError(f"lse: expected a contiguous fp32 tensor {shape[:3]} on {cache.device}")
-    if ws.get_device() != cache.index:
-        raise ValueError(f"ws: expected a buffer on {cache.device}")
+        raise ValueError(f"lse: expected a contiguous fp32 tensor {tuple(shape[:3])} on {cache.device}")
+    if ws.get_device() != cache.index or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous buffer on {cache.device}")
     a = dg_kv4_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                    _kv4_ints(cache, rows, c.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],
-                    shape[1], code, int(bool(causal)), c.d_head ** -0.5 if scale is None else scale)
-    _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), _ptr(ws),
-                                                ws.numel() * ws.element_size(), _kv4_stream(cache, stream)))
+                    _kv4_ints(cache, rows, cache.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],
+                    shape[1], code, 1 if causal else 0, cache.d_head ** -0.5 if scale is None else scale)
+    _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), ws.data_ptr(), ws.nbytes,
+                                                _kv4_stream(cache, stream)))
 
 
 def dg_store_prefix_kv4(seqs: Seqs, seq, cache: Kv4Cache, slot):

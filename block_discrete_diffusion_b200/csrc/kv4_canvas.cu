@@ -499,9 +499,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
     auto q_chunk = [&](int row, int i) {         // 16-byte chunk i of the warp's row
       return reinterpret_cast<uint4*>(qtile + (i / 8) * 16384 + row * 128 + (((i & 7) ^ (row & 7)) << 4));
     };
-    // The warp's rows of Q as they are into their places, dh / 8 lanes a row.  (All rows that the tensor has: those behind
-    // the sequence's last one are set to zero when they are scaled.)
-    auto load_q = [&](int seq, int head, int row0) {
+    // The warp's rows of Q as they are into their places, dh / 8 lanes a row; of n query rows.  (Those behind the last one
+    // are set to zero when the others are scaled.)
+    auto load_q = [&](int seq, int head, int row0, int n) {
       constexpr int kLanes = DH / 8, kRows = 32 / kLanes;
       const int first = x * 128 + (warp & 3) * 32 + lane / kLanes;   // row of round 0, then kRows further each
       int qj = group_row(a, row0 + first), qg = row0 + first - qj * G;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const T* q = static_cast<const T*>(a.q) + seq * a.q_seq + (head * G) * a.q_head + lane % kLanes * 8;
 #pragma unroll 4
       for (int i = 0; i < 32 / kRows; ++i) {
-        if (qj < a.rows) cp_async16(q_chunk(i * kRows + lane / kLanes, lane % kLanes), q + qj * a.q_row + qg * a.q_head);
+        if (qj < n) cp_async16(q_chunk(i * kRows + lane / kLanes, lane % kLanes), q + qj * a.q_row + qg * a.q_head);
         qj += dj;
         qg += dg;
         if (qg >= G) {
@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
     };
     bool met = false;                            // the cluster, before its rows are written
     if constexpr (Cluster) {
-      load_q(unit.seq, unit.head, unit.tile * kKv4ManyTile);   // (while the lengths are on their way)
+      // (while the walker reads the length too)
+      load_q(unit.seq, unit.head, unit.tile * kKv4ManyTile, a.n_rows ? min(a.n_rows[unit.seq], a.rows) : a.rows);
     }
     uint32_t n_step = 0;                         // steps of this tile so far
     while (tasks.next(pc)) {
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       if (steps > 0) {
         // Q to fp16 in its place, times a power of two, a thread a row.  (The S products of the last piece, which read these
         // rows, are complete: this warp has read the last S)
-        if constexpr (!Cluster) load_q(pc.seq, pc.head, pc.row0);
+        if constexpr (!Cluster) load_q(pc.seq, pc.head, pc.row0, pc.n);
         cp_async_wait_all();
         __syncwarp();
         uint4 w[DH / 8];

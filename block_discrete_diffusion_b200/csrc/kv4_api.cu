@@ -98,8 +98,8 @@ struct Plan {
   static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
 };
 
-// Rows of a KV head up to which the few-rows form runs whatever the lengths (32 sequences of 8192 positions, 8 KV heads:
-// 8 rows 68 us, 32 rows 208 us, 64 rows 402 us; the other form 258 to 262 us for any of them).
+// Rows of a KV head up to which the few-rows form runs whatever the lengths (32 sequences of 8192 positions, 8 KV
+// heads: 8 rows 68 us, 32 rows 208 us, 64 rows 402 us; the other form 258 to 262 us for any of them).
 constexpr int kFewRows = 32;
 
 Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
@@ -108,12 +108,12 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
   const long long group_rows = (long long)rows * (n_q / c->n_kv);
   const int few_ctas = sms * kv4_few_ctas(c->d_head);
   // A cluster for each unit where the sequences cannot be long: one launch and no parts in memory (one token behind
-  // 577 positions: 11.7 -> 7.0 us).  Longer units want more warps than a cluster of such CTAs has (32768 positions: 21.2 us
-  // on the line, 24.8 in clusters of 16 CTAs, 24.3 of 12-warp CTAs that fill an SM), and units of different lengths
-  // leave SMs idle: from about 24 pages a CTA on that costs more than the second launch.  Where the many-rows form
-  // stands on the other side, its clusters win from 10 to 12 pages a CTA on (128 rows, 4 pages a CTA 8.3 us, 12.2 in the other
-  // form; 10 pages 12.5 and 13.5; 24 pages 20.3 and 14.7; 48 rows, 6 pages 11.6 and 11.4, 12 pages 15.8 and 14.5; heads of
-  // 64, 128 rows, 12 pages 13.3 and 13.9).
+  // 577 positions: 11.7 -> 7.0 us).  Longer units want more warps than a cluster of such CTAs has (32768 positions:
+  // 21.2 us on the line, 24.8 in clusters of 16 CTAs, 24.3 of 12-warp CTAs that fill an SM), and units of different
+  // lengths leave SMs idle: from about 24 pages a CTA on that costs more than the second launch.  Where the many-rows
+  // form stands on the other side, its clusters win from 10 to 12 pages a CTA on (128 rows, 4 pages a CTA 8.3 us,
+  // 12.2 in the other form; 10 pages 12.5 and 13.5; 24 pages 20.3 and 14.7; 48 rows, 6 pages 11.6 and 11.4, 12 pages
+  // 15.8 and 14.5; heads of 64, 128 rows, 12 pages 13.3 and 13.9).
   const long long units = (group_rows + kKv4FewTile - 1) / kKv4FewTile * c->n_kv * c->n_seq;
   int n = kKv4MaxCluster;
   while (n > 1 && units * n > few_ctas) n /= 2;
@@ -126,9 +126,10 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     p.row_bytes = 4 * (size_t)c->d_head;
   } else {
     p.n_ctas = sms;                                // one CTA holds an SM
-    // Clusters here too where all units' run at once and none is long (see above).  Eight CTAs of a GPC's SMs at most, and
-    // fewer clusters than SMs / size would give: with 16 clusters of 8 the last ones waited (2304 positions, one canvas,
-    // in an earlier form of the join: 36.9 us; 16 clusters of 4 22.6 us, the line 23.8 us; 600 positions 30.5, 15.7, 19.6).
+    // Clusters here too where all units' run at once and none is long (see above).  Eight CTAs of a GPC's SMs at
+    // most, and fewer clusters than SMs / size would give: with 16 clusters of 8 the last ones waited (2304
+    // positions, one canvas, in an earlier form of the join: 36.9 us; 16 clusters of 4 22.6 us, the line 23.8 us; 600
+    // positions 30.5, 15.7, 19.6).
     const long long many = (group_rows + kKv4ManyTile - 1) / kKv4ManyTile * c->n_kv * c->n_seq;
     int m = many <= sms ? kKv4MaxManyCluster : 0;
     while (m > 0 && many > kv4_many_clusters(c->d_head, m)) --m;

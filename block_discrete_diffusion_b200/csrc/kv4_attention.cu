@@ -32,11 +32,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 // distributed shared memory in the same launch; others divide the line of all units evenly (kv4_attention.cuh) and
 // join in a second launch.
 //
-// 4 warps; a warp takes every fourth page of the CTA's piece of a unit.  It keeps a ring of whole blocks in shared memory (one bulk copy each: a block is contiguous), dequantises them into
-// m16n8k16 fragments and multiplies S = K Q^T and O^T += V^T P^T: positions and channels are the 16-wide
-// side, the rows the 8-wide one, so a tile of 8 rows wastes no tensor work, and a row's statistics lie with the same
-// lanes in S and in O^T.  Bound by the cache's bytes: mma.sync is enough, since 8 rows x 2 operations a value
-// stay far below its rate.
+// 4 warps; a warp takes every fourth page of the CTA's piece of a unit.  It keeps a ring of whole blocks in shared
+// memory (one bulk copy each: a block is contiguous), dequantises them into m16n8k16 fragments and multiplies S = K
+// Q^T and O^T += V^T P^T: positions and channels are the 16-wide side, the rows the 8-wide one, so a tile of 8 rows
+// wastes no tensor work, and a row's statistics lie with the same lanes in S and in O^T.  Bound by the cache's bytes:
+// mma.sync is enough, since 8 rows x 2 operations a value stay far below its rate.
 constexpr int kFewWarps = 4;               // warps of a CTA; three CTAs an SM keep 24 blocks in flight
 constexpr int kFewStages = 2;
 constexpr int kMaxCluster = kKv4MaxCluster;
@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
     Piece pc;
     while (stretch.next(pc)) {
       work(pc);
+      fence_proxy_async_smem();            // (rows were joined in the rings: before the next copies into them)
       if (!__syncthreads_and(ok)) break;   // (the rings are free again; a warp that gave up has told)
     }
   }
@@ -433,8 +434,8 @@ __device__ __forceinline__ Pieces pieces_of(const Kv4View& c, const Kv4Attn& a, 
   return p;
 }
 
-// few rows: a CTA for each (sequence, row, head), whose warps share out the pieces (one token behind 32768 positions has 56 a
-// row: one warp walking them spent 4 us waiting for its loads)
+// few rows: a CTA for each (sequence, row, head), whose warps share out the pieces (one token behind 32768 positions
+// has 56 a row: one warp walking them spent 4 us waiting for its loads)
 constexpr int kMergeWarps = 8;
 template <int DH, typename T>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv4_merge_few_kernel(Kv4View c, Kv4Attn a) {

@@ -7,10 +7,10 @@
 // thread's loads are under way before the first is used (32 KB of rows a CTA).
 //
 // Pages.  The book (lengths, reference counts, tables) is a few hundred KB at most and its updates depend on one
-// another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left
-// as a list of (from, to) for a second launch over the whole GPU (whose CTAs are placed while the first runs; one launch
-// whose other CTAs wait for the list measured 33.5 us instead of 23.5 for 32 copies of 2.2 MB).  Nothing changes when a call cannot be
-// carried out whole: the error word tells.
+// another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left as a
+// list of (from, to) for a second launch over the whole GPU (whose CTAs are placed while the first runs; one launch
+// whose other CTAs wait for the list measured 33.5 us instead of 23.5 for 32 copies of 2.2 MB).  Nothing changes when
+// a call cannot be carried out whole: the error word tells.
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -73,8 +73,8 @@ __device__ __forceinline__ void merge_words(uint4* p, uint4 v, uint32_t mask) {
   *p = v;
 }
 
-// 8 channels of two neighbouring positions of a transposed V (positions side by side, channels `stride` elements apart): each
-// word holds both positions of a channel
+// 8 channels of two neighbouring positions of a transposed V (positions side by side, channels `stride` elements
+// apart): each word holds both positions of a channel
 template <typename T>
 __device__ __forceinline__ void load_pairs(const void* base, long long at, long long stride, float (&x0)[8],
                                            float (&x1)[8]) {
@@ -86,8 +86,9 @@ __device__ __forceinline__ void load_pairs(const void* base, long long at, long 
   }
 }
 
-// Rows [len - n, len) of every sequence into (Write) or out of its pages.  2 DH threads: each takes two half blocks of
-// K (8 channels of two positions) and one of V (8 channels of four positions).  Whole: one sequence's prefix, V transposed.
+// Rows [len - n, len) of every sequence into (Write) or out of its pages.  2 DH threads: each takes two half blocks
+// of K (8 channels of two positions) and one of V (8 channels of four positions).  Whole: one sequence's prefix, V
+// transposed.
 template <int DH, typename T, bool Write, bool Whole>
 __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, Kv4Rows r) {
   using F = Kv4<DH>;

@@ -6,7 +6,8 @@
 //                P = 2^(S - m) in fp16 back into S's columns of TMEM, running sum, the finished row out
 //   warps 8-11   dequantise: pages' blocks from a ring of three in shared memory to fp16 K and V tiles in the 128-byte
 //                swizzled layout of the tensor core, a ring of eight
-//   warp 12      issues the products of tile 0, warp 15 those of tile 1: S = Q K^T of a step, O += P V of the step two before
+//   warp 12      issues the products of tile 0, warp 15 those of tile 1: S = Q K^T of a step, O += P V of the step two
+//                before
 //   warp 13      walks the CTA's stretch and hands its pieces to the others, up to four ahead
 //   warp 14      copies the pages' blocks into their ring, one bulk copy each
 //
@@ -16,15 +17,16 @@
 // P as the tensor core's operand in TMEM and not in shared memory takes 128 KB off the 384 KB that 128 positions
 // cost there; the blocks come by bulk copies because loads into registers were waited for by each tile's proxy fence.
 //
-// A call whose units fit the SMs in clusters runs one for each unit, whose CTAs each join a share of its rows, and the second
-// launch falls away.  A row goes from TMEM into its place in the Q tile and from there in one piece into the shared memory of the CTA that
-// joins it.  Such a call is a chain of latencies (one canvas behind 2048 positions: 19.1 us, 6 of them its six steps), so Q
-// is copied asynchronously while the lengths are read, a thread scales a row of it from registers (1.5 us less than
-// sixteen rounds of loads, shuffles and stores), and no index is divided by a variable.
+// A call whose units fit the SMs in clusters runs one for each unit, whose CTAs each join a share of its rows, and
+// the second launch falls away.  A row goes from TMEM into its place in the Q tile and from there in one piece into
+// the shared memory of the CTA that joins it.  Such a call is a chain of latencies (one canvas behind 2048 positions:
+// 19.1 us, 6 of them its six steps), so Q is copied asynchronously while the lengths are read, a thread scales a row
+// of it from registers (1.5 us less than sixteen rounds of loads, shuffles and stores), and no index is divided by a
+// variable.
 //
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
-// positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in the same
-// order, which only renames registers.  The running maximum is lazy: O and the sum are rescaled when a row's
+// positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in
+// the same order, which only renames registers.  The running maximum is lazy: O and the sum are rescaled when a row's
 // maximum has grown by more than 2^8, so P stays below 2^8.
 #include <math.h>
 
@@ -38,7 +40,8 @@ constexpr int kManyThreads = 512;
 // Registers a thread after the split of the launch's 4 x 128: two softmax groups, the dequantisers, the issuers.
 constexpr int kRegsSoftmax = 152, kRegsDequant = 120, kRegsIssue = 88;
 constexpr int kRegsLaunch = 128;
-static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * kRegsLaunch, "register split above what the CTA was launched with");
+static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * kRegsLaunch,
+              "register split above what the CTA was launched with");
 constexpr int kRing = 8;       // fp16 tiles of 64 positions
 constexpr int kRaw = 3;        // pages' blocks
 constexpr float kLazy = 8.f;   // log2 units
@@ -48,10 +51,11 @@ template <int DH>
 struct ManySmem {
   static constexpr uint32_t kQ = 128u * DH * 2u;       // a Q tile
   static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
-  static constexpr size_t kBytes = 1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024 + 4 * kMaxManyCluster;
+  static constexpr size_t kBytes =
+      1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024 + 4 * kMaxManyCluster;
   static_assert(kBytes <= 232448, "shared memory budget");
   static_assert(kRing * kTile + kRaw * Kv4<DH>::kBytes >= (256u + kMaxManyCluster - 1) * DH * 4u,
-                "the rings hold the rows in fp32 that a cluster's CTA joins: of n CTAs, each at most 1/n of 256, rounded up");
+                "the rings hold the rows in fp32 that a cluster's CTA joins: of each of n, 1/n of 256, rounded up");
 };
 
 // A piece of work as the roles need it.
@@ -321,8 +325,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&bars->kv_full[b]);
-            // The block's slot is free only now that all its values have been used: an arrival behind the loads alone let the
-            // next copy meet loads of V that were still under way
+            // The block's slot is free only now that all its values have been used: an arrival behind the loads alone
+            // let the next copy meet loads of V that were still under way
             mbar_arrive(&bars->raw_empty[slot]);
           }
           ++item;
@@ -499,8 +503,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
     auto q_chunk = [&](int row, int i) {         // 16-byte chunk i of the warp's row
       return reinterpret_cast<uint4*>(qtile + (i / 8) * 16384 + row * 128 + (((i & 7) ^ (row & 7)) << 4));
     };
-    // The warp's rows of Q as they are into their places, dh / 8 lanes a row; of n query rows.  (Those behind the last one
-    // are set to zero when the others are scaled.)
+    // The warp's rows of Q as they are into their places, dh / 8 lanes a row; of n query rows.  (Those behind the
+    // last one are set to zero when the others are scaled.)
     auto load_q = [&](int seq, int head, int row0, int n) {
       constexpr int kLanes = DH / 8, kRows = 32 / kLanes;
       const int first = x * 128 + (warp & 3) * 32 + lane / kLanes;   // row of round 0, then kRows further each
@@ -534,8 +538,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const int limit = row_limit(SeqView{pc.len, pc.n}, j, a.causal);
       float sl2 = 0.f;
       if (steps > 0) {
-        // Q to fp16 in its place, times a power of two, a thread a row.  (The S products of the last piece, which read these
-        // rows, are complete: this warp has read the last S)
+        // Q to fp16 in its place, times a power of two, a thread a row.  (The S products of the last piece, which
+        // read these rows, are complete: this warp has read the last S)
         if constexpr (!Cluster) load_q(pc.seq, pc.head, pc.row0, pc.n);
         cp_async_wait_all();
         __syncwarp();
@@ -639,9 +643,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const float lse2 = some ? m_used + log2f(l) : -INFINITY;
       T* dst = static_cast<T*>(a.out) + pc.seq * a.o_seq + j * a.o_row + h * a.o_head;
       const size_t at = (size_t)pc.slot * kKv4ManyTile + x * 128 + r;
-      // A part for a bf16 output in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; for an fp16
-      // output, whose own rounding that is, in fp32.  16-byte chunks of the tile's rows lie side by side, so that a
-      // warp's stores and the merge's loads are contiguous
+      // A part for a bf16 output in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; for an
+      // fp16 output, whose own rounding that is, in fp32.  16-byte chunks of the tile's rows lie side by side, so
+      // that a warp's stores and the merge's loads are contiguous
       constexpr int kPer = kPartPer<T>;   // channels of a chunk
       auto chunk_of = [](const float(&o)[32], int e) {
         if constexpr (kPer == 4)
@@ -653,9 +657,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       };
       uint4* part = static_cast<uint4*>(a.part_o) + (size_t)pc.slot * kKv4ManyTile * (DH / kPer) + x * 128 + r;
       if (Cluster && unit.n > 1) {
-        // Each CTA of the cluster joins its share of the rows.  A row goes into this warp's part of the Q tile, whose products
-        // are complete, and from there in one piece to the CTA that joins it: as the lanes hold the rows, a store would
-        // meet a line for each lane
+        // Each CTA of the cluster joins its share of the rows.  A row goes into this warp's part of the Q tile, whose
+        // products are complete, and from there in one piece to the CTA that joins it: as the lanes hold the rows, a
+        // store would meet a line for each lane
         const int per = (pc.nr + unit.n - 1) / unit.n, owner = min((x * 128 + r) / per, unit.n - 1);
         const int place = unit.rank * per + x * 128 + r - owner * per;
         const uint32_t to = dsmem_map(smem_u32(kv_s) + place * (16 * DH / kPer), owner);
@@ -727,7 +731,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   __syncthreads();
   if (warp == 12) tmem_dealloc(tmem, 512);
   if (Cluster && unit.n > 1) {
-    // every CTA of the cluster has its share of the unit's rows from all of them, and joins it, a thread for a 16-byte chunk at a time
+    // every CTA of the cluster has its share of the unit's rows from all of them, and joins it, a thread for a
+    // 16-byte chunk at a time
     cluster_sync();
     const int n = unit.n, nr = bars->task[0].nr;                 // (0: the unit has no rows)
     const int per = (nr + n - 1) / n, first = unit.rank * per, mine = min(per, nr - first);
@@ -816,8 +821,8 @@ cudaError_t launch_many(const Kv4View& c, int layer, const Kv4Attn& a, cudaStrea
   if (e != cudaSuccess) return e;
   if (a.cluster) {
     const int tiles = (a.rows * a.group + kKv4ManyTile - 1) / kKv4ManyTile;
-    return launch_k(kv4_attend_many_kernel<DH, T, true>, dim3(tiles, c.n_kv, c.n_seq * a.cluster), dim3(kManyThreads), kBytes, st,
-                    a.cluster, c, layer, a);
+    return launch_k(kv4_attend_many_kernel<DH, T, true>, dim3(tiles, c.n_kv, c.n_seq * a.cluster), dim3(kManyThreads),
+                    kBytes, st, a.cluster, c, layer, a);
   }
   return launch_k(kv4_attend_many_kernel<DH, T, false>, dim3(a.n_ctas), dim3(kManyThreads), kBytes, st, 1, c, layer, a);
 }

@@ -98,6 +98,8 @@ struct Plan {
   static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
 };
 
+constexpr size_t kWorkspaceSlack = 256;   // the parts begin at a multiple of it
+
 // Rows of a KV head up to which the few-rows form runs whatever the lengths (32 sequences of 8192 positions, 8 KV
 // heads: 8 rows 68 us, 32 rows 208 us, 64 rows 402 us; the other form 258 to 262 us for any of them).
 constexpr int kFewRows = 32;
@@ -226,7 +228,7 @@ DG_API dg_status dg_kv4_read(const dg_kv4_cache* c, int layer, const dg_kv4_rows
 
 DG_API size_t dg_kv4_attend_workspace_bytes(const dg_kv4_cache* c, int n_q, int rows) {
   if (shape_error(c) || n_q <= 0 || n_q % c->n_kv || n_q > 8192 || rows <= 0 || rows > 65536) return 0;
-  return plan_of(c, n_q, rows).bytes(c) + 256;
+  return plan_of(c, n_q, rows).bytes(c) + kWorkspaceSlack;
 }
 
 DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_attn* a, void* ws, size_t ws_bytes,
@@ -243,9 +245,8 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return bad(fn, "scale must be positive and finite");
   if ((a->q_seq | a->q_row | a->q_head | a->o_seq | a->o_row | a->o_head) & 7)
     return bad(fn, "strides must be multiples of 8 elements");
-  if (!ws || ws_bytes < dg_kv4_attend_workspace_bytes(c, a->n_q, a->rows))
-    return bad(fn, "workspace too small", DG_ERR_CAPACITY);
   const Plan p = plan_of(c, a->n_q, a->rows);
+  if (!ws || ws_bytes < p.bytes(c) + kWorkspaceSlack) return bad(fn, "workspace too small", DG_ERR_CAPACITY);
   Kv4Attn k{};
   k.q = a->q;
   k.out = a->out;

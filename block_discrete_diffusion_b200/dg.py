@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -150,11 +151,12 @@ def lib():
         L.dg_kv4_fork.argtypes = [C, c_void_p, c_void_p, c_int, c_void_p]
         L.dg_kv4_free.argtypes = [C, c_void_p, c_int, c_void_p]
         L.dg_kv4_compact.argtypes = [C, c_void_p]
-        L.dg_kv4_append.argtypes = [C, c_int, P(dg_kv4_rows), c_void_p]
-        L.dg_kv4_read.argtypes = [C, c_int, P(dg_kv4_rows), c_void_p]
+        # (their structs: packed bytes, or ctypes.byref of the class)
+        L.dg_kv4_append.argtypes = [C, c_int, c_void_p, c_void_p]
+        L.dg_kv4_read.argtypes = [C, c_int, c_void_p, c_void_p]
         L.dg_kv4_attend_workspace_bytes.argtypes = [C, c_int, c_int]
         L.dg_kv4_attend_workspace_bytes.restype = c_size_t
-        L.dg_kv4_attend.argtypes = [C, c_int, P(dg_kv4_attn), c_void_p, c_size_t, c_void_p]
+        L.dg_kv4_attend.argtypes = [C, c_int, c_void_p, c_void_p, c_size_t, c_void_p]
         L.dg_kv4_error.argtypes = [C, c_void_p, P(c_int)]
         L.dg_store_prefix_kv4.argtypes = [c_void_p, c_int, C, c_int]
         L.dg_load_prefix_kv4.argtypes = [c_void_p, c_int, c_int, C, c_int]
@@ -407,14 +409,19 @@ def dg_kv4_book_bytes(c) -> int:
     return int(lib().dg_kv4_book_bytes(ctypes.byref(getattr(c, "c", c))))
 
 
-# the current stream's handle without building a Stream object (3 us of a call's 15)
+# A small call's time is the host's, so: the current stream's handle without building a Stream object (3 us), the
+# device's index without the wrapper's checks (the cache's tensors have initialised CUDA), structs packed at once.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_pack_rows = struct.Struct("@PPqqqqqqPii")      # dg_kv4_rows
+_pack_attn = struct.Struct("@PPPPqqqqqqiiiif4x")   # dg_kv4_attn
+assert _pack_rows.size == ctypes.sizeof(dg_kv4_rows) and _pack_attn.size == ctypes.sizeof(dg_kv4_attn)
 
 
 def _kv4_stream(cache, stream):
     """The stream's handle; the kernels run on the current device, so the cache has to lie there."""
-    if cache.index != torch.cuda.current_device():
+    if cache.index != _current_device():
         raise ValueError(f"the cache lies on {cache.device}, the current device is cuda:{torch.cuda.current_device()}")
     if stream is None:
         return _current_raw_stream(cache.index)
@@ -422,27 +429,28 @@ def _kv4_stream(cache, stream):
 
 
 def _kv4_ints(cache, t, n, what):
-    """An int32 argument of n values on the cache's device (None stays None)."""
+    """The address of an int32 argument of n values on the cache's device (0 for None)."""
     if t is None:
-        return None
-    if t.dtype != torch.int32 or t.get_device() != cache.index or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
+        return 0
+    if t.dtype != torch.int32 or t.shape != (n,) or t.get_device() != cache.index or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous int32 values on {cache.device}")
     return t.data_ptr()
 
 
 def _kv4_tensor(cache, t, shape, what, dtype=None):
     """A rows argument: its type's code and its strides; channels lie side by side."""
-    code = _KV4_DTYPES.get(t.dtype)
-    if code is None or (dtype is not None and t.dtype != dtype):
+    own = t.dtype
+    code = _KV4_DTYPES.get(own)
+    if code is None or (dtype is not None and own != dtype):
         raise ValueError(f"{what}: expected bf16 or fp16, the same for every tensor of the call")
     if t.shape != shape or t.get_device() != cache.index:
         raise ValueError(f"{what}: expected shape {tuple(shape)} on {cache.device}, got {tuple(t.shape)} on {t.device}")
-    s = t.stride()
-    if s[3] != 1:
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise ValueError(f"{what}: channels must be contiguous")
-    if (s[0] | s[1] | s[2]) & 7:   # the stride of a dimension of one says nothing
-        s = tuple(0 if n == 1 else k for n, k in zip(shape, s))
-    return code, s
+    if (s0 | s1 | s2) & 7:   # the stride of a dimension of one says nothing
+        s0, s1, s2 = (0 if n == 1 else k for n, k in zip(shape, (s0, s1, s2)))
+    return code, s0, s1, s2
 
 
 def dg_kv4_init(cache: Kv4Cache, stream=None):
@@ -473,11 +481,11 @@ def dg_kv4_compact(cache: Kv4Cache, stream=None):
 
 def _kv4_rows(fn, cache, layer, k, v, rows, stream):
     shape = (cache.n_seq, k.shape[1] if k.dim() == 4 else -1, cache.n_kv, cache.d_head)
-    code, ks = _kv4_tensor(cache, k, shape, "k")
-    _, vs = _kv4_tensor(cache, v, shape, "v", k.dtype)
-    r = dg_kv4_rows(k.data_ptr(), v.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                    _kv4_ints(cache, rows, cache.n_seq, "rows"), shape[1], code)
-    _check(fn, getattr(lib(), fn)(cache.ref, layer, ctypes.byref(r), _kv4_stream(cache, stream)))
+    code, k0, k1, k2 = _kv4_tensor(cache, k, shape, "k")
+    _, v0, v1, v2 = _kv4_tensor(cache, v, shape, "v", k.dtype)
+    r = _pack_rows.pack(k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, _kv4_ints(cache, rows, cache.n_seq, "rows"),
+                        shape[1], code)
+    _check(fn, getattr(lib(), fn)(cache.ref, layer, r, _kv4_stream(cache, stream)))
 
 
 def dg_kv4_append(cache: Kv4Cache, layer, k, v, rows=None, stream=None):
@@ -502,17 +510,18 @@ def dg_kv4_attend(cache: Kv4Cache, layer, q, out, ws, rows=None, lse=None, scale
     shape = q.shape
     if len(shape) != 4 or shape[0] != cache.n_seq or shape[3] != cache.d_head:
         raise ValueError(f"q: expected [{cache.n_seq}, T, n_q, {cache.d_head}], got {tuple(shape)}")
-    code, qs = _kv4_tensor(cache, q, shape, "q")
-    _, os_ = _kv4_tensor(cache, out, shape, "out", q.dtype)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()
-                            or lse.get_device() != cache.index):
-        raise ValueError(f"lse: expected a contiguous fp32 tensor {tuple(shape[:3])} on {cache.device}")
+    code, q0, q1, q2 = _kv4_tensor(cache, q, shape, "q")
+    _, o0, o1, o2 = _kv4_tensor(cache, out, shape, "out", q.dtype)
+    n, T, n_q, _ = shape
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, T, n_q) or lse.get_device() != cache.index
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected a contiguous fp32 tensor {(n, T, n_q)} on {cache.device}")
     if ws.get_device() != cache.index or not ws.is_contiguous():
         raise ValueError(f"ws: expected a contiguous buffer on {cache.device}")
-    a = dg_kv4_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                    _kv4_ints(cache, rows, cache.n_seq, "rows"), qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], shape[2],
-                    shape[1], code, 1 if causal else 0, cache.d_head ** -0.5 if scale is None else scale)
-    _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, ctypes.byref(a), ws.data_ptr(), ws.nbytes,
+    a = _pack_attn.pack(q.data_ptr(), out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                        _kv4_ints(cache, rows, n, "rows"), q0, q1, q2, o0, o1, o2, n_q, T, code, 1 if causal else 0,
+                        cache.d_head ** -0.5 if scale is None else scale)
+    _check("dg_kv4_attend", lib().dg_kv4_attend(cache.ref, layer, a, ws.data_ptr(), ws.nbytes,
                                                 _kv4_stream(cache, stream)))
 
 

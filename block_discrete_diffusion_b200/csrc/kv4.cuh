@@ -81,7 +81,10 @@ __device__ __forceinline__ uint32_t ue5m3_scale(float amax) {
 // Quotient x / s on the grid of 2^-16, from r = 1 / s to 2^-22.  The product errs by less than 2^-18 and an exact
 // quotient of an 11-bit value by a 4-bit scale is either on a border between two codes (a multiple of 1/4) or at
 // least 2^-13 away from it: on the grid every border case is met exactly, and ties go to the even code.
-__device__ __forceinline__ float on_grid(float x, float r) { return __fadd_rn(__fmaf_rn(x, r, 192.f), -192.f); }
+// (two at once)
+__device__ __forceinline__ uint64_t on_grid2(uint64_t x, uint64_t r) {
+  return fadd_f32x2(ffma_f32x2(x, r, pack_f32x2(192.f, 192.f)), pack_f32x2(-192.f, -192.f));
+}
 
 // four pairs of quotients as the e2m1 bytes of a word (first of a pair in the low nibble), nearest, ties to even,
 // beyond 6 saturating

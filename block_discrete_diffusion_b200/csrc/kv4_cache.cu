@@ -51,8 +51,13 @@ __device__ __forceinline__ uint32_t to_quotients(float (&x)[8]) {
   const uint32_t byte = ue5m3_scale(amax);
   const float s = ue5m3_to_f32(byte);
   const float r = s > 0.f ? fast_rcp(s) : 0.f;
+  const uint64_t rr = pack_f32x2(r, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = on_grid(x[i], r);
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t y = on_grid2(pack_f32x2(x[i], x[i + 1]), rr);
+    x[i] = lo_f32(y);
+    x[i + 1] = hi_f32(y);
+  }
   return byte;
 }
 

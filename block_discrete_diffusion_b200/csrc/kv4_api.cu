@@ -131,11 +131,13 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     // Clusters here too where all units' run at once and none is long (see above).  Eight CTAs of a GPC's SMs at
     // most, and fewer clusters than SMs / size would give: with 16 clusters of 8 the last ones waited (2304
     // positions, one canvas, in an earlier form of the join: 36.9 us; 16 clusters of 4 22.6 us, the line 23.8 us; 600
-    // positions 30.5, 15.7, 19.6).
+    // positions 30.5, 15.7, 19.6).  One canvas behind 2000 positions 19.2 us, 23.3 on the line; behind 9000 40.2 and
+    // 45.0; two behind 6000, 24 pages a CTA, 40.8 and 49.8.  (Sequences of different lengths leave SMs idle, so not
+    // up to where equal ones break even, 50 pages a CTA and more.)
     const long long many = (group_rows + kKv4ManyTile - 1) / kKv4ManyTile * c->n_kv * c->n_seq;
     int m = many <= sms ? kKv4MaxManyCluster : 0;
     while (m > 0 && many > kv4_many_clusters(c->d_head, m)) --m;
-    if (m > 0 && c->max_pages <= (c->n_seq == 1 ? 24 : 16) * m) p.cluster = m;
+    if (m > 0 && c->max_pages <= (c->n_seq == 1 ? 32 : 24) * m) p.cluster = m;
     p.min_share = 1;
     p.tile = kKv4ManyTile;
     p.row_bytes = 4 * (size_t)c->d_head;           // (parts for a bf16 output take half of it)

@@ -537,12 +537,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const int j = group_row(a, rr), h = pc.head * G + rr - j * G;
       const int limit = row_limit(SeqView{pc.len, pc.n}, j, a.causal);
       float sl2 = 0.f;
+      // (The S products of the last piece, which read these rows, are complete: this warp has read the last S)
+      if (!Cluster && steps > 0) load_q(pc.seq, pc.head, pc.row0, pc.n);
+      // A cluster's copies were started before the piece was known: also a CTA without steps waits for its own before
+      // its rows go through the Q tile
+      cp_async_wait_all();
+      __syncwarp();
       if (steps > 0) {
-        // Q to fp16 in its place, times a power of two, a thread a row.  (The S products of the last piece, which
-        // read these rows, are complete: this warp has read the last S)
-        if constexpr (!Cluster) load_q(pc.seq, pc.head, pc.row0, pc.n);
-        cp_async_wait_all();
-        __syncwarp();
+        // Q to fp16 in its place, times a power of two, a thread a row
         uint4 w[DH / 8];
         uint32_t top[4] = {0, 0, 0, 0};   // largest magnitudes: 16-bit floats in the order of their bits
 #pragma unroll

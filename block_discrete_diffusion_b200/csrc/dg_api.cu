@@ -370,6 +370,7 @@ struct dg_seqs {
   uint8_t* ws;
   // typed workspace views
   int *err, *seqP;
+  int refused = 0;   // code of a load that was refused, for dg_device_error (not in err, where it would end waits)
   float *x, *ml, *rlog, *gate, *y, *logits, *samp, *hsamp, *splitk;
   __nv_bfloat16* opart;   // attention key-split partial outputs
   __nv_bfloat16 *xn, *q, *attn, *xp, *hb;
@@ -1023,8 +1024,11 @@ DG_API dg_status dg_load_prefix(dg_seqs* s, int seq, int P, const void* const* h
 
 namespace {
 
-// One sequence's committed prefix into or out of a 4-bit cache, layer by layer.
-dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_cache* cache, int slot, bool store) {
+// One sequence's committed prefix into or out of a 4-bit cache, layer by layer; *refused: the device-side code of a
+// load that moved nothing, 0 otherwise.
+dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_cache* cache, int slot, bool store,
+                      int* refused) {
+  *refused = 0;
   if (!s) return fail(DG_ERR_INVALID_ARG, "%s: seqs is null", fn);
   const dg_status st = kv4_check_cache(fn, cache);
   if (st != DG_OK) return st;
@@ -1036,6 +1040,15 @@ dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_c
   if (P < 0 || P + kCanvas > s->max_ctx) return fail(DG_ERR_CAPACITY, "%s: prefix %d + canvas exceeds max_ctx", fn, P);
   if (P > (long long)cache->max_pages * DG_KV4_PAGE)
     return fail(DG_ERR_CAPACITY, "%s: prefix %d exceeds the cache's %d pages a sequence", fn, P, cache->max_pages);
+  const Kv4View view = kv4_view(cache);
+  // What a load brings becomes the sequence's length here on the host, so the host has to know that it fits.  (A store's
+  // rows are checked by the kernels that move them; a prefix without rows has none.)
+  if (!store || P == 0) CK(kv4_check_prefix(view, slot, P, s->st));
+  if (!store) {
+    CK(cudaMemcpyAsync(refused, view.head + KV4_WORD_PREFIX, sizeof(int), cudaMemcpyDeviceToHost, s->st));
+    CK(cudaStreamSynchronize(s->st));
+    if (*refused) return DG_OK;
+  }
   const size_t per_seq = (size_t)c.n_kv * s->max_ctx * c.d_head;
   for (int l = 0; l < c.n_layers && P > 0; ++l) {
     Kv4Rows r{};
@@ -1046,7 +1059,7 @@ dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_c
     r.k_head = r.v_head = (long long)s->max_ctx * c.d_head;
     r.rows = P;
     r.only = slot + 1;
-    CK(kv4_rows(kv4_view(cache), l, r, store, s->st));
+    CK(kv4_rows(view, l, r, store, s->st));
   }
   return DG_OK;
 }
@@ -1056,13 +1069,19 @@ dg_status move_prefix(const char* fn, dg_seqs* s, int seq, int P, const dg_kv4_c
 DG_API dg_status dg_store_prefix_kv4(dg_seqs* s, int seq, const dg_kv4_cache* cache, int slot) {
   NvtxRange nvtx_range("dg_store_prefix_kv4");
   const int P = s && seq >= 0 && seq < s->n_seq ? s->P[seq] : 0;
-  return move_prefix("dg_store_prefix_kv4", s, seq, P, cache, slot, true);
+  int refused;
+  return move_prefix("dg_store_prefix_kv4", s, seq, P, cache, slot, true, &refused);
 }
 
 DG_API dg_status dg_load_prefix_kv4(dg_seqs* s, int seq, int P, const dg_kv4_cache* cache, int slot) {
   NvtxRange nvtx_range("dg_load_prefix_kv4");
-  const dg_status st = move_prefix("dg_load_prefix_kv4", s, seq, P, cache, slot, false);
+  int refused;
+  const dg_status st = move_prefix("dg_load_prefix_kv4", s, seq, P, cache, slot, false, &refused);
   if (st != DG_OK) return st;
+  if (refused) {
+    if (!s->refused) s->refused = refused;
+    return DG_OK;
+  }
   CK(add_to_P(s->seqP, seq, 1, P - s->P[seq], s->st));
   s->P[seq] = P;
   return DG_OK;
@@ -1584,6 +1603,10 @@ DG_API dg_status dg_device_error(dg_seqs* s, int* h_code) {
   int code = 0;
   CK(cudaMemcpy(&code, s->err, sizeof(int), cudaMemcpyDeviceToHost));
   CK(cudaMemset(s->err, 0, sizeof(int)));
+  if (!code) {
+    code = s->refused;
+    s->refused = 0;
+  }
   *h_code = code;
   if (code) return fail(DG_ERR_DEVICE, "device-side error code %d", code);
   return DG_OK;

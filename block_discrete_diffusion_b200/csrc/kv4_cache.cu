@@ -301,6 +301,26 @@ cudaError_t launch_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool writ
                   0, st, 1, c, layer, r);
 }
 
+__device__ __forceinline__ int pages_of(long long len) { return (int)((len + kPage - 1) / kPage); }
+
+// One CTA.  (P is at most max_pages pages.)
+constexpr int kCheckThreads = 256;
+__global__ void __launch_bounds__(kCheckThreads) kv4_check_prefix_kernel(Kv4View c, int slot, int P) {
+  pdl_trigger();
+  pdl_wait();
+  const bool fits = c.lens[slot] == P;
+  int bad = 0;
+  for (int i = threadIdx.x; fits && i < pages_of(P); i += kCheckThreads) {
+    const int page = c.table[(size_t)slot * c.max_pages + i];
+    bad |= page < 0 || page >= c.n_pages;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x != 0) return;
+  const int code = !fits ? DEV_ERR_BAD_COUNT : bad ? DEV_ERR_BAD_INDEX : 0;
+  c.head[KV4_WORD_PREFIX] = code;
+  if (code) report_error(c.head, code);
+}
+
 // ---------------------------------------------------------------------------------------------
 // the book
 // ---------------------------------------------------------------------------------------------
@@ -336,8 +356,6 @@ __device__ int block_scan(int v, int* total) {
   __syncthreads();
   return before;
 }
-
-__device__ __forceinline__ int pages_of(long long len) { return (int)((len + kPage - 1) / kPage); }
 
 // What a sequence needs to grow by `count`: pages it has, whether it copies its last one, pages to take.
 struct Growth {
@@ -621,6 +639,10 @@ cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, 
                   : launch_rows<128, __nv_bfloat16>(c, layer, r, write, st);
   return r.fp16 ? launch_rows<64, __half>(c, layer, r, write, st)
                 : launch_rows<64, __nv_bfloat16>(c, layer, r, write, st);
+}
+
+cudaError_t kv4_check_prefix(const Kv4View& c, int slot, int P, cudaStream_t st) {
+  return launch_k(kv4_check_prefix_kernel, dim3(1), dim3(kCheckThreads), 0, st, 1, c, slot, P);
 }
 
 cudaError_t kv4_extend(const Kv4View& c, const int32_t* counts, int n_sms, cudaStream_t st) {

@@ -13,13 +13,14 @@ namespace dg {
 struct Kv4View {
   uint8_t* pool;         // [n_layers][n_pages][n_kv][72 d_head] bytes
   int32_t* head;         // [0] error code, [1] moves of the last page call, [2] live pages of the last compaction,
-                         // [3] error code of a wait (apart, since a wait gives up once it is set)
+                         // [3] error code of a wait (apart, since a wait gives up once it is set),
+                         // [4] what the last check of a prefix found
   int32_t *lens, *refs, *table;
   int32_t *move_src, *move_dst, *map;   // scratch of the page calls, n_pages words each
   int n_layers, n_kv, dh, n_pages, n_seq, max_pages;
 };
 
-enum : int { KV4_WORD_ERR = 0, KV4_WORD_MOVES = 1, KV4_WORD_LIVE = 2, KV4_WORD_WAIT = 3, KV4_HEAD_WORDS = 16 };
+enum : int { KV4_WORD_ERR = 0, KV4_WORD_MOVES = 1, KV4_WORD_LIVE = 2, KV4_WORD_WAIT = 3, KV4_WORD_PREFIX = 4, KV4_HEAD_WORDS = 16 };
 
 // K / V rows of an append or a read: element (seq, row, head, c) at seq * s_seq + row * s_row + head * s_head + c.
 struct Kv4Rows {
@@ -34,6 +35,8 @@ struct Kv4Rows {
 };
 
 cudaError_t kv4_rows(const Kv4View& c, int layer, const Kv4Rows& r, bool write, cudaStream_t st);
+// Whether sequence `slot` has P positions, on pages of the pool: 0 or the code that is recorded, in KV4_WORD_PREFIX.
+cudaError_t kv4_check_prefix(const Kv4View& c, int slot, int P, cudaStream_t st);
 
 // page bookkeeping; each is one launch on the book, extend and compact with a second one that moves pages
 cudaError_t kv4_extend(const Kv4View& c, const int32_t* counts, int n_sms, cudaStream_t st);

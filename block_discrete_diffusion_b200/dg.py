@@ -532,7 +532,8 @@ def dg_store_prefix_kv4(seqs: Seqs, seq, cache: Kv4Cache, slot):
 
 
 def dg_load_prefix_kv4(seqs: Seqs, seq, P, cache: Kv4Cache, slot):
-    """The prefix of length P that the cache's sequence slot holds as sequence seq's."""
+    """The prefix of length P that the cache's sequence slot holds as sequence seq's.  Waits for the stream; a slot of
+    another length changes nothing and is what dg_kv4_error and dg_device_error tell next."""
     _kv4_stream(cache, seqs.stream)
     _check("dg_load_prefix_kv4", lib().dg_load_prefix_kv4(seqs.handle, seq, P, cache.ref, slot))
 

@@ -369,8 +369,9 @@ dg_status dg_kv4_attend(const dg_kv4_cache *c, int layer, const dg_kv4_attn *a, 
  * prefix [0, P) of sequence `seq`, every layer, into the cache's sequence `slot`, which has length P (dg_kv4_extend)
  * and pages without other owners; dg_load_prefix_kv4 installs the prefix that `slot` holds, of length P, as sequence
  * `seq`'s (replacing its cache content, as dg_load_prefix does).  The cache has the model's layers, KV heads and
- * d_head.  Enqueued on the handle's stream; a length other than P is recorded in the cache's book (code 8) and moves
- * nothing. */
+ * d_head.  Both run on the handle's stream; a length other than P is recorded in the cache's book (code 8) and moves
+ * nothing.  A load waits for the stream once, to see that the slot fits: one that does not leaves the sequence as it was,
+ * its length included, and its code (8, or 5 for a page out of range) is what dg_device_error tells next. */
 dg_status dg_store_prefix_kv4(dg_seqs *s, int seq, const dg_kv4_cache *cache, int slot);
 dg_status dg_load_prefix_kv4(dg_seqs *s, int seq, int P, const dg_kv4_cache *cache, int slot);
 

@@ -1,9 +1,15 @@
 """The paged 4-bit cache on the GPU where it can go wrong: ends of the number ranges, calls that are refused on the device,
 shares of work without pages.  The reference and the tolerance are those of test_gpu_kv4.py, where nothing else is said."""
+import dataclasses
+
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv4 import BF16, attend, make
+import kv4_reference as R
+import synthetic
+from block_discrete_diffusion_b200 import dg
+from test_gpu_kv4 import BF16, attend, blocks, dev, kv_views, make
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +28,75 @@ def test_canvas_with_fewer_pages_than_its_cluster_has_ctas(lens, causal):
         c = make(2, 128, lens, seed=seed)
         attend(c, 2, 256, BF16, causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
         attend(c, 2, 256, BF16, rows=[130], causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
+
+
+# ---------------------------------------------------------------------------------------------
+# a sequence set's prefixes
+# ---------------------------------------------------------------------------------------------
+def step_logits(s, cfg):
+    """The logits of a canvas step behind the set's prefixes."""
+    n, prm = s.n_seq * 256, dg.sampler_params(cfg.vocab, seed=3)
+    out = torch.empty(n, cfg.vocab, device="cuda")
+    ids, commit = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda")
+    dg.dg_canvas_init(s, prm, ids, commit)
+    dg.dg_canvas_step(s, prm, ids, commit, torch.empty(n, device="cuda"),
+                      torch.empty(s.n_seq, dtype=torch.int32, device="cuda"), logits=out)
+    return out
+
+
+def test_a_refused_load_leaves_the_sequence_as_it_was():
+    """A slot of another length, an empty one, one with a page that is none: neither the rows nor the length change, the steps
+    go on behind the old prefix, and both objects tell."""
+    cfg = synthetic.TINY
+    model = dg.dg_model_create(cfg, synthetic.make_model_weights(cfg, 0, device="cuda"))
+    s = dg.dg_seqs_create(model, 2, 512)
+    dg.dg_prefill(s, synthetic.make_ids(107, cfg.vocab, 1, device="cuda"), [100, 7])
+    c = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, cfg.d_head, 6, 3, 4)
+    dg.dg_kv4_extend(c, dev([99, 0, 130]))
+    c.table[2, 1] = 6
+    want = step_logits(s, cfg)
+    kv, pool = s.kv.clone(), c.pool.clone()
+    for P, slot, code in ((98, 0, 8), (100, 0, 8), (0, 0, 8), (64, 1, 8), (130, 2, 5)):
+        dg.dg_load_prefix_kv4(s, 0, P, c, slot)
+        assert dg.dg_seqs_get_state(s)[0] == [100, 7] and torch.equal(kv, s.kv)
+        assert dg.dg_kv4_error(c) == code and dg.dg_kv4_error(c) == 0
+        assert dg.dg_device_error(s) == code and dg.dg_device_error(s) == 0
+    assert torch.equal(want, step_logits(s, cfg)) and dg.dg_device_error(s) == 0
+    dg.dg_load_prefix_kv4(s, 0, 0, c, 1)                # a prefix without rows is one
+    assert dg.dg_seqs_get_state(s)[0] == [0, 7]
+    dg.dg_store_prefix_kv4(s, 0, c, 1)
+    assert dg.dg_kv4_error(c) == 0 and dg.dg_device_error(s) == 0
+    dg.dg_store_prefix_kv4(s, 0, c, 0)                  # ... that slot 0 does not hold
+    assert dg.dg_kv4_error(c) == 8 and torch.equal(pool, c.pool)
+
+
+@pytest.mark.parametrize("P", [1, 65, 1001, 4096])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_prefixes_of_both_head_sizes_from_any_sequence(dh, P):
+    """Prefixes of unequal lengths wait in the cache and come back to other sequences: their rows are the quantised ones, and what
+    lies behind them is left alone."""
+    cfg = dataclasses.replace(synthetic.TINY, d_head=dh)
+    model = dg.dg_model_create(cfg, synthetic.make_model_weights(cfg, 0, device="cuda"))
+    s, back = dg.dg_seqs_create(model, 3, 4608), dg.dg_seqs_create(model, 3, 4608)
+    g = torch.Generator(device="cuda").manual_seed(P)
+    lens = [P // 2 + 1, P, 200]
+    for i, n in enumerate(lens):
+        x = torch.randn((2, cfg.n_layers, n, cfg.n_kv, dh), generator=g, device="cuda").to(BF16)
+        dg.dg_load_prefix(s, i, n, list(x[0]), list(x[1]))
+    c = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, dh, 150, 3, 64)
+    dg.dg_kv4_extend(c, dev(lens[::-1]))
+    back.kv.view(BF16).fill_(3)
+    for i in range(3):
+        dg.dg_store_prefix_kv4(s, i, c, 2 - i)
+        dg.dg_load_prefix_kv4(back, (i + 1) % 3, lens[i], c, 2 - i)
+    assert dg.dg_kv4_error(c) == 0 and dg.dg_seqs_get_state(back)[0] == [lens[2], lens[0], lens[1]]
+    (k, v), (bk, bv) = kv_views(s), kv_views(back)
+    for i, n in enumerate(lens):
+        at = (i + 1) % 3
+        for layer in range(cfg.n_layers):
+            for x, got, held in zip((k[layer, i, :, :n], v[layer, i, :, :, :n].transpose(1, 2)),
+                                    (bk[layer, at, :, :n], bv[layer, at, :, :, :n].transpose(1, 2)), blocks(c, layer, 2 - i)):
+                want = R.value(*R.quantise(x.double().cpu().numpy()))
+                np.testing.assert_array_equal(held, want)
+                np.testing.assert_array_equal(got.double().cpu().numpy(), want)
+        assert bool((bk[:, at, :, n:] == 3).all()) and bool((bv[:, at, :, :, n:] == 3).all())

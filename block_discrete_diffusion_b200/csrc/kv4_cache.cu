@@ -116,12 +116,16 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
   const int start = len - n;
   const int lp = start / kPage + blockIdx.x;
   if ((long long)lp * kPage >= len) return;
-  const int page = c.table[(size_t)seq * c.max_pages + lp];
-  if (page < 0 || page >= c.n_pages) {
-    if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
-    return;
+  const int32_t* table = c.table + (size_t)seq * c.max_pages;
+  const int page = min(max(table[lp], 0), c.n_pages - 1);   // (looked at below; in the pool whatever it is)
+  // All of the call's pages of this sequence are looked at by each of its CTAs before its first store, so that the rows
+  // move whole or not at all (512 pages cost two more loads a thread, which are under way beside those of the rows)
+  int bad = 0;
+  for (int i = start / kPage + threadIdx.x; (long long)i * kPage < len; i += kThreads) {
+    const int p = table[i];
+    const bool in = p >= 0 && p < c.n_pages;
+    bad |= !in || (Write && c.refs[p] != 1);   // (a page with other owners is nobody's to write)
   }
-  const int owners = Write ? c.refs[page] : 1;   // (looked at before the first store)
   uint8_t* block = c.pool + (((size_t)layer * c.n_pages + page) * c.n_kv + head) * F::kBytes;
   const int lo = max(start - lp * kPage, 0), hi = min(len - lp * kPage, kPage);   // positions of this page
   const long long row0 = (long long)lp * kPage - start;                          // row of the page's position 0
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = in[e] ? load8<T>(r.v, v_at(e)) : zero;
     }
-    if (owners != 1) {   // a page with other owners is nobody's to write
+    if (__syncthreads_or(bad)) {
       if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
       return;
     }
@@ -223,17 +227,26 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
       if (u == 0) *v_scale = s_mask == 0xffffffffu ? s : (*v_scale & ~s_mask) | (s & s_mask);
     }
   } else {
-    if (!__any_sync(0xffffffffu, in0[0] || in1[0] || in0[1] || in1[1] || v_mask)) return;
+    const bool some = __any_sync(0xffffffffu, in0[0] || in1[0] || in0[1] || in1[1] || v_mask);
     uint2 kw[2];
     float ks0[2], ks1[2];
+    uint4 vw;
+    uint32_t vs;
+    if (some) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      kw[i] = *k_words[i];
-      ks0[i] = ue5m3_to_f32(k_scale[i][0]);
-      ks1[i] = ue5m3_to_f32(k_scale[i][F::kH]);
+      for (int i = 0; i < 2; ++i) {
+        kw[i] = *k_words[i];
+        ks0[i] = ue5m3_to_f32(k_scale[i][0]);
+        ks1[i] = ue5m3_to_f32(k_scale[i][F::kH]);
+      }
+      vw = *v_words;
+      vs = *v_scale;
     }
-    const uint4 vw = *v_words;
-    const uint32_t vs = *v_scale;
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+      return;
+    }
+    if (!some) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w[2] = {kw[i].x, kw[i].y};

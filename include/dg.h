@@ -333,8 +333,8 @@ typedef struct {
   int rows, dtype;
 } dg_kv4_rows;
 
-/* Quantise the rows into the sequences' last positions of one layer (dg_kv4_extend made room for them).  A
- * page with other owners is not written. */
+/* Quantise the rows into the sequences' last positions of one layer (dg_kv4_extend made room for them).  A sequence
+ * of which the rows would meet a page with other owners is not written, its other pages neither. */
 dg_status dg_kv4_append(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);
 /* The values that the sequences' last positions of one layer stand for (exact in both types). */
 dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);

@@ -9,7 +9,7 @@ import torch
 import kv4_reference as R
 import synthetic
 from block_discrete_diffusion_b200 import dg
-from test_gpu_kv4 import BF16, attend, blocks, dev, kv_views, make
+from test_gpu_kv4 import BF16, FP16, attend, blocks, dev, kv_views, make
 
 pytestmark = pytest.mark.gpu
 
@@ -28,6 +28,53 @@ def test_canvas_with_fewer_pages_than_its_cluster_has_ctas(lens, causal):
         c = make(2, 128, lens, seed=seed)
         attend(c, 2, 256, BF16, causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
         attend(c, 2, 256, BF16, rows=[130], causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
+
+
+@pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("n_pages", [3, 300])
+def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):
+    """One page of several that has another owner, or is none, keeps all rows of its sequence where they are, in and out; the
+    other sequences' rows move."""
+    lens = [64 * n_pages - 10, 70, 64 * n_pages]
+    T = 64 * n_pages - 30
+    c = make(2, dh, lens, n_layers=2)
+    rows = dev([T, 70, T])
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn((3, T, 2, dh), generator=g, device="cuda").to(dtype) for _ in range(2))
+    table, refs, pool = c.table.clone(), c.refs.clone(), c.pool.clone()
+    whole = c.pool.view(2, -1, 2 * 72 * dh)
+    for at in (0, n_pages // 2, n_pages - 1):
+        for kind in ("shared", "missing", "negative"):
+            if kind == "shared":
+                c.refs[table[0, at]] = 2
+            else:
+                c.table[0, at] = c.c.n_pages if kind == "missing" else -1
+            c.pool.copy_(pool)
+            dg.dg_kv4_append(c, 1, k, v, rows=rows)
+            assert dg.dg_kv4_error(c) == 5
+            mine = table[0, :n_pages].long()
+            before = pool.view(2, -1, 2 * 72 * dh)
+            assert torch.equal(whole[:, mine], before[:, mine]) and torch.equal(whole[0], before[0])
+            c.refs.copy_(refs)
+            c.pool.copy_(pool)
+            dg.dg_kv4_append(c, 1, k, v, rows=rows * dev([0, 1, 1]))
+            assert dg.dg_kv4_error(c) == 0
+            want = c.pool.clone()
+            c.pool.copy_(pool)
+            if kind == "shared":
+                c.refs[table[0, at]] = 2
+            dg.dg_kv4_append(c, 1, k, v, rows=rows)     # the others' rows are those of a call without the first
+            assert dg.dg_kv4_error(c) == 5 and torch.equal(want, c.pool)
+            k2, v2 = torch.full_like(k, 3), torch.full_like(v, 3)
+            dg.dg_kv4_read(c, 1, k2, v2, rows=rows)
+            kk, vv = (x[2, :T] for x in (k2, v2))
+            assert not bool((kk == 3).all()) and not bool((vv == 3).all())
+            if kind == "shared":                        # (a shared page may be read)
+                assert dg.dg_kv4_error(c) == 0 and not bool((k2[0] == 3).all())
+            else:
+                assert dg.dg_kv4_error(c) == 5 and bool((k2[0] == 3).all()) and bool((v2[0] == 3).all())
+            c.table.copy_(table)
+            c.refs.copy_(refs)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -100,3 +147,19 @@ def test_prefixes_of_both_head_sizes_from_any_sequence(dh, P):
                 np.testing.assert_array_equal(held, want)
                 np.testing.assert_array_equal(got.double().cpu().numpy(), want)
         assert bool((bk[:, at, :, n:] == 3).all()) and bool((bv[:, at, :, :, n:] == 3).all())
+
+
+def test_a_store_onto_shared_pages_changes_nothing():
+    cfg = synthetic.TINY
+    model = dg.dg_model_create(cfg, synthetic.make_model_weights(cfg, 0, device="cuda"))
+    s = dg.dg_seqs_create(model, 1, 512)
+    x = torch.randn((2, cfg.n_layers, 200, cfg.n_kv, cfg.d_head), device="cuda").to(BF16)
+    dg.dg_load_prefix(s, 0, 200, list(x[0]), list(x[1]))
+    c = dg.dg_kv4_cache(cfg.n_layers, cfg.n_kv, cfg.d_head, 8, 2, 4)
+    dg.dg_kv4_extend(c, dev([100, 0]))
+    dg.dg_kv4_fork(c, dev([0]), dev([1]))
+    dg.dg_kv4_extend(c, dev([100, 0]))                  # its first page is still the other's too
+    c.pool.random_(0, 256)
+    before = c.pool.clone()
+    dg.dg_store_prefix_kv4(s, 0, c, 0)
+    assert dg.dg_kv4_error(c) == 5 and torch.equal(before, c.pool)

@@ -119,13 +119,18 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
   const int32_t* table = c.table + (size_t)seq * c.max_pages;
   const int page = min(max(table[lp], 0), c.n_pages - 1);   // (looked at below; in the pool whatever it is)
   // All of the call's pages of this sequence are looked at by each of its CTAs before its first store, so that the rows
-  // move whole or not at all (512 pages cost two more loads a thread, which are under way beside those of the rows)
-  int bad = 0;
-  for (int i = start / kPage + threadIdx.x; (long long)i * kPage < len; i += kThreads) {
-    const int p = table[i];
-    const bool in = p >= 0 && p < c.n_pages;
-    bad |= !in || (Write && c.refs[p] != 1);   // (a page with other owners is nobody's to write)
-  }
+  // move whole or not at all.  Whole CTA, once its loads of rows are under way
+  auto refused = [&] {
+    int bad = 0;
+    for (int i = start / kPage + threadIdx.x; (long long)i * kPage < len; i += kThreads) {
+      const int p = table[i];
+      const bool in = p >= 0 && p < c.n_pages;
+      bad |= !in || (Write && c.refs[p] != 1);   // (a page with other owners is nobody's to write)
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
+    return bad != 0;
+  };
   uint8_t* block = c.pool + (((size_t)layer * c.n_pages + page) * c.n_kv + head) * F::kBytes;
   const int lo = max(start - lp * kPage, 0), hi = min(len - lp * kPage, kPage);   // positions of this page
   const long long row0 = (long long)lp * kPage - start;                          // row of the page's position 0
@@ -189,10 +194,7 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = in[e] ? load8<T>(r.v, v_at(e)) : zero;
     }
-    if (__syncthreads_or(bad)) {
-      if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
-      return;
-    }
+    if (refused()) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!__any_sync(0xffffffffu, in0[i] || in1[i])) continue;   // (single tokens: most warps have nothing)
@@ -242,11 +244,7 @@ __global__ void __launch_bounds__(2 * DH) kv4_rows_kernel(Kv4View c, int layer, 
       vw = *v_words;
       vs = *v_scale;
     }
-    if (__syncthreads_or(bad)) {
-      if (threadIdx.x == 0) report_error(c.head, DEV_ERR_BAD_INDEX);
-      return;
-    }
-    if (!some) return;
+    if (refused() || !some) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w[2] = {kw[i].x, kw[i].y};

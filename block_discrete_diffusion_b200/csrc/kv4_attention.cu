@@ -3,7 +3,8 @@
 // o = softmax(scale q k^T) v over the positions [0, len) of a sequence (causal: row j of n sees positions up to
 // len - n + j), with k and v dequantised on the way to the tensor cores.  Statistics and sums are in fp32; the
 // operands are fp16: k and v are exact in it (6 significant bits), q is made exact by a power of two per row,
-// and p in [0, 1] is rounded once, by 2^-11 of itself at most.
+// and p is rounded once, by 2^-11 of itself, or by 2^-32 (many rows) or 2^-40 (few) of the row's largest where that is
+// more (reference_of); the row's sum takes it unrounded.
 #include <math.h>
 
 #include "kv4_attention.cuh"
@@ -40,6 +41,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 constexpr int kFewWarps = 4;               // warps of a CTA; three CTAs an SM keep 24 blocks in flight
 constexpr int kFewStages = 2;
 constexpr int kMaxCluster = kKv4MaxCluster;
+constexpr int kFewShift = 15;              // p in [0, 2^15]: its reference is the largest score met so far, less this
 
 template <int DH>
 struct FewSmem {
@@ -224,8 +226,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
         for (int e = 0; e < 2; ++e) {
           top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 4));
           top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 8));
-          top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 16));
+          top[e] = reference_of<kFewShift>(max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], 16)));
         }
+        // (references follow the largest scores in the same order)
         const float n0 = max_nan(m[0], top[0]), n1 = max_nan(m[1], top[1]);   // (a NaN score makes its row NaN)
         if (__any_sync(0xffffffffu, n0 != m[0] || n1 != m[1])) {
           const float f0 = n0 == m[0] ? 1.f : fast_exp2(m[0] - n0), f1 = n1 == m[1] ? 1.f : fast_exp2(m[1] - n1);
@@ -332,7 +335,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
         v0 /= den;
         v1 /= den;
       }
-      const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(den);
+      // (the shift in both terms, so that their rounding is that of the score and of a sum from its largest)
+      const float lse2 = top == -INFINITY ? -INFINITY : top + kFewShift + log2f(den * (1.f / (1 << kFewShift)));
       const int r = r0 + row, j = group_row(a, r), h = head * G + r - j * G;
       if (Cluster && unit.n > 1) {
         *reinterpret_cast<float2*>(part + row * DH + ch) = make_float2(v0, v1);

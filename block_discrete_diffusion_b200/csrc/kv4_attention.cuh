@@ -224,6 +224,15 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// The reference of a row's weights: p = 2^(s - reference), in fp16 for the product with v.  A reference 2^-Shift below
+// the row's largest score uses the upper part of fp16's range, so that small weights, of which a long context may have
+// many, keep their bits down to 2^-(14 + Shift) of the largest and a value down to 2^-(25 + Shift).  Shift is left out of
+// sums and statistics by itself, since these count from the reference.  Beyond 2^20 fp32 scores lie too far apart for it.
+template <int Shift>
+__device__ __forceinline__ float reference_of(float top) {
+  return fabsf(top) < 1048576.f ? top - (float)Shift : top;
+}
+
 // Channels in a 16-byte chunk of a part of the many-rows form: fp16 for a bf16 output, fp32 for an fp16 one.
 template <typename T>
 constexpr int kPartPer = std::is_same<T, __half>::value ? 4 : 8;

@@ -27,7 +27,7 @@
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
 // positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in
 // the same order, which only renames registers.  The running maximum is lazy: O and the sum are rescaled when a row's
-// maximum has grown by more than 2^8, so P stays below 2^8.
+// maximum has grown by more than 2^8; it is taken 2^7 low, so P stays below 2^15 and has most of fp16's range.
 #include <math.h>
 
 #include "kv4_attention.cuh"
@@ -45,6 +45,7 @@ static_assert(2 * kRegsSoftmax + kRegsDequant + kRegsIssue <= 4 * kRegsLaunch,
 constexpr int kRing = 8;       // fp16 tiles of 64 positions
 constexpr int kRaw = 3;        // pages' blocks
 constexpr float kLazy = 8.f;   // log2 units
+constexpr int kManyShift = 7;  // log2 of P's largest value where the reference has just followed (reference_of)
 constexpr int kMaxManyCluster = kKv4MaxManyCluster;
 
 template <int DH>
@@ -591,7 +592,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
 #pragma unroll
         for (int e = 0; e < 64; e += 2) top[e / 2 & 3] = max3(top[e / 2 & 3], s[e], s[e + 1]);
         // the reference follows when the maximum has grown by more than kLazy (the first finite one: above -inf)
-        const float tmax = fmaxf(max3(top[0], top[1], top[2]), top[3]) * sl2;
+        const float tmax = reference_of<kManyShift>(fmaxf(max3(top[0], top[1], top[2]), top[3]) * sl2);
         const bool grow = tmax > m_used + kLazy;
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? tmax : m_used;
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       }
       const bool some = steps > 0 && l != 0.f;   // (a row may see nothing; a NaN sum goes through)
       const float inv = some ? 1.f / l : 0.f;
-      const float lse2 = some ? m_used + log2f(l) : -INFINITY;
+      const float lse2 = some ? m_used + kManyShift + log2f(l * (1.f / (1 << kManyShift))) : -INFINITY;
       T* dst = static_cast<T*>(a.out) + pc.seq * a.o_seq + j * a.o_row + h * a.o_head;
       const size_t at = (size_t)pc.slot * kKv4ManyTile + x * 128 + r;
       // A part for a bf16 output in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; for an

@@ -30,6 +30,67 @@ def test_canvas_with_fewer_pages_than_its_cluster_has_ctas(lens, causal):
         attend(c, 2, 256, BF16, rows=[130], causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
 
 
+# ---------------------------------------------------------------------------------------------
+# attention at the ends of the number ranges
+# ---------------------------------------------------------------------------------------------
+# rows of a call and pages of a table: single tokens and canvases, each in clusters and along the line
+FORMS = [(1, None), (1, 3000), (256, None), (256, 3000)]
+
+
+def cache_of(k, v, table=None):
+    """A cache with the rows k, v [positions, n_kv, dh] in one sequence, quantised; free pages before, between and behind."""
+    n, n_kv, dh = k.shape
+    pages = -(-n // 64)
+    c = dg.dg_kv4_cache(1, n_kv, dh, pages + 2, 1, table or pages)
+    c.pool.fill_(255)
+    dg.dg_kv4_extend(c, dev([n]))
+    dg.dg_kv4_append(c, 0, k[None], v[None])
+    return c
+
+
+def run(c, q, scale, rows=None, causal=False):
+    T, n_q = q.shape[1:3]
+    out, lse = torch.full_like(q, 3), torch.full(q.shape[:3], 7.0, device="cuda")
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, n_q, T), dtype=torch.uint8, device="cuda")
+    dg.dg_kv4_attend(c, 0, q, out, ws, rows=rows, lse=lse, scale=scale, causal=causal)
+    assert dg.dg_kv4_error(c) == 0
+    return out, lse
+
+
+def check_tails(c, q, out, lse, scale):
+    """As check of test_gpu_kv4.py, with less room below: a weight is kept to 2^-32 of the row's largest, a joined part to 2^-39 of
+    its row's largest magnitude."""
+    dh, n = c.c.d_head, int(c.lens[0])
+    half = torch.finfo(q.dtype).eps / 2
+    k, v = blocks(c, 0, 0)
+    o, want_lse, absum, reach, vsum = R.attention(q[0].double().cpu().numpy(), k, v, [n] * q.shape[1], scale)
+    delta = 2 * (dh / 16) * 2.0 ** -21 * reach + 2.0 ** -21
+    tol = absum * (2 * 2.0 ** -11 + delta[..., None] + 2.0 ** -17) * (1 + half) + half * np.abs(o) + 2.0 ** -32 * vsum
+    tol += 2.0 ** -39 * absum.max(-1, keepdims=True)
+    if q.dtype == FP16:
+        tol += 2.0 ** -25              # steps of a small output
+    err = np.abs(out[0].double().cpu().numpy() - o)
+    assert (err <= tol).all(), float((err / tol).max())
+    d = np.abs(lse[0].double().cpu().numpy() - want_lse)
+    assert (d <= delta + 2.0 ** -22 * np.abs(want_lse)).all(), float(d.max())
+
+
+@pytest.mark.parametrize("T,table", FORMS)
+@pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("gap", [15.0, 20.0, 24.5, 25.5, 28.0])
+@pytest.mark.parametrize("at", [0, 300, 699])
+def test_a_long_tail_behind_one_dominant_key(T, table, dh, dtype, gap, at):
+    """One position's weight is 2^gap of each other's, and its value is zero: the output is the tail's."""
+    g = torch.Generator(device="cuda").manual_seed(int(gap))
+    k, v = torch.zeros((700, 2, dh), device="cuda"), torch.rand((700, 2, dh), generator=g, device="cuda") * 5e4
+    k[at, :, 0], v[at] = 6, 0
+    q = torch.zeros((1, T, 4, dh), device="cuda").to(dtype)
+    q[..., 0] = 1
+    scale = float(np.float32(gap * np.log(2) / 6))
+    c = cache_of(k.to(dtype), v.to(dtype), table)
+    check_tails(c, q, *run(c, q, scale), scale)
+
+
 @pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
 @pytest.mark.parametrize("n_pages", [3, 300])
 def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):

@@ -46,6 +46,7 @@ constexpr int kRing = 8;       // fp16 tiles of 64 positions
 constexpr int kRaw = 3;        // pages' blocks
 constexpr float kLazy = 8.f;   // log2 units
 constexpr int kManyShift = 7;  // log2 of P's largest value where the reference has just followed (reference_of)
+constexpr float kFar = 1048576.f;   // a reference from here on is subtracted from rounded scores
 constexpr int kMaxManyCluster = kKv4MaxManyCluster;
 
 template <int DH>
@@ -573,6 +574,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         if (lane == 0) mbar_arrive(&bars->q_full[x]);
       }
       float m_used = -INFINITY, l = 0.f;
+      bool far = false;                          // the reference is kFar or more
       for (int i = 0; i < steps; ++i, ++n_step) {
         const uint32_t buf = n_step & 1;
         const uint32_t t_s = tmem + lane_off + x * 128 + 64 * buf;
@@ -594,11 +596,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         // the reference follows when the maximum has grown by more than kLazy (the first finite one: above -inf)
         const float tmax = reference_of<kManyShift>(fmaxf(max3(top[0], top[1], top[2]), top[3]) * sl2);
         const bool grow = tmax > m_used + kLazy;
-        if (__any_sync(0xffffffffu, grow)) {
+        float factor = sl2;
+        if (__any_sync(0xffffffffu, grow || far)) {
           const float m_new = grow ? tmax : m_used;
           const float alpha = grow && m_used != -INFINITY ? fast_exp2(m_used - m_new) : 1.f;
           l *= alpha;
           m_used = m_new;
+          far = fabsf(m_used) >= kFar && m_used != -INFINITY;
+          if (__any_sync(0xffffffffu, far)) {
+            // The reference is a rounded product; this far out the exact products of the multiply-add below lie up to
+            // half a unit of it off, which is more than P has room for.  So the scores are rounded as it was
+            factor = 1.f;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) s[e] *= sl2;
+          }
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
             // O holds the steps before this one once the last of their products is complete
             ok = ok && warp_wait(&bars->pv_done[x][buf ^ 1], ((n_step - 1) >> 1) & 1, err);
@@ -617,7 +628,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         // P over S, in V's order: words 4 ch .. 4 ch + 3 (chunk ch = 2 t + b) are the pairs t of the 8-position groups
         // 4 b .. 4 b + 3.  (Nothing seen yet: every score is -inf, p is 0.)
         const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-        const uint64_t sl2x2 = pack_f32x2(sl2, sl2), negm2 = pack_f32x2(-m_ref, -m_ref);
+        const uint64_t sl2x2 = pack_f32x2(factor, factor), negm2 = pack_f32x2(-m_ref, -m_ref);
         uint64_t sum[2] = {0, 0};
         uint32_t pk[32];
 #pragma unroll

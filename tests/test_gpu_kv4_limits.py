@@ -91,6 +91,45 @@ def test_a_long_tail_behind_one_dominant_key(T, table, dh, dtype, gap, at):
     check_tails(c, q, *run(c, q, scale), scale)
 
 
+@pytest.mark.parametrize("T,table", FORMS)
+@pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
+@pytest.mark.parametrize("power", [10, 17, 18, 20, 22, 24, 26, 27, 28, 30, 40, 100])
+def test_scores_beyond_their_own_accuracy(T, table, dh, dtype, power):
+    """Scores near 2^power, where fp32 numbers lie far apart, and further apart than they do: the largest one's value comes out, and
+    rows beside it whose scores are small are what they are without it."""
+    g = torch.Generator(device="cuda").manual_seed(power)
+    n = 500
+    k = torch.randint(-4, 5, (n, 2, dh), generator=g, device="cuda").float()
+    v = torch.randn((n, 2, dh), generator=g, device="cuda")
+    best, worst = 77, 401                       # 6 in channel 0, and -6; others are at most 4
+    k[best, :, 0], k[worst, :, 0] = 6, -6
+    c = cache_of(k.to(dtype), v.to(dtype), table)
+    q = torch.zeros((1, T, 4, dh), device="cuda").to(dtype)
+    up = 2.0 ** (power - 4)
+    # heads 0 and 2 have large scores, 1 small ones beside those of 0, 3 none
+    if dtype == BF16:
+        q[..., 0, 0], q[..., 2, 0], q[..., 1, 0], scale = up, -up, 2.0 ** -3, 1.0
+    else:
+        q[..., 0, 0], q[..., 2, 0], q[..., 1, 0], scale = 2.0 ** 5, -2.0 ** 5, 2.0 ** -24, up / 2 ** 5
+    out, lse = run(c, q, scale)
+    _, vv = blocks(c, 0, 0)
+    # The weight is rounded to fp16, by 2^-11, and the sum is not. A value has 6 bits, and a bf16 output's 8 are not reached by
+    # that rounding (and a joined part's, 2^-11 too); an fp16 output is off by it and its own
+    room = 0 if dtype == BF16 else 2.0 ** -10
+    for h, pos in ((0, best), (2, worst)):
+        want = np.broadcast_to(vv[h // 2, pos], (T, dh))
+        assert (np.abs(out[0, :, h].double().cpu().numpy() - want) <= room * np.abs(want)).all()
+        assert bool(((lse[0, :, h].double() - 6 * up).abs() <= 2.0 ** -22 * 6 * up).all())
+    if dtype == BF16 or power <= 20:
+        small = q.clone()
+        small[..., 0::2, :] = 0
+        alone, alone_lse = run(c, small, scale)
+        check_tails(c, small, alone, alone_lse, scale)
+        # (each is off by the tolerances above at most: a step of the output, and P's rounding of values up to 6)
+        x, y = out[..., 1::2, :].float(), alone[..., 1::2, :].float()
+        assert bool(((x - y).abs() <= torch.finfo(dtype).eps * y.abs() + 2 * 6 * 2.0 ** -11).all())
+
+
 @pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
 @pytest.mark.parametrize("n_pages", [3, 300])
 def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):

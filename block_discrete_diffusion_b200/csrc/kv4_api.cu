@@ -93,8 +93,10 @@ int current_sms() {
 struct Plan {
   bool few;
   int cluster, n_ctas, min_share;
-  size_t tile, row_bytes;   // rows of a workspace slot, bytes of a row in it
-  size_t bytes(const dg_kv4_cache* c) const { return line_bytes(c) + 2 * (size_t)n_ctas * tile * (row_bytes + 4); }
+  size_t tile, row_bytes, stat_bytes;   // rows of a workspace slot, bytes of a row in it, of its lse and power
+  size_t bytes(const dg_kv4_cache* c) const {
+    return line_bytes(c) + 2 * (size_t)n_ctas * tile * (row_bytes + stat_bytes);
+  }
   static size_t line_bytes(const dg_kv4_cache* c) { return (16 + 8 * (size_t)c->n_seq + 255) & ~size_t(255); }
 };
 
@@ -126,6 +128,7 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     p.min_share = 4;                               // a page for each warp
     p.tile = kKv4FewTile;
     p.row_bytes = 4 * (size_t)c->d_head;
+    p.stat_bytes = 4;
   } else {
     p.n_ctas = sms;                                // one CTA holds an SM
     // Clusters here too where all units' run at once and none is long (see above).  Eight CTAs of a GPC's SMs at
@@ -141,6 +144,7 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
     p.min_share = 1;
     p.tile = kKv4ManyTile;
     p.row_bytes = 4 * (size_t)c->d_head;           // (parts for a bf16 output take half of it)
+    p.stat_bytes = 8;
   }
   return p;
 }

@@ -540,9 +540,10 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
   const Pieces p = pieces_of<kKv4ManyTile, kKv4ManyStep>(c, a, seq, v, head, r / kKv4ManyTile);
   if (p.c0 == p.c1) return;
   const size_t row = r % kKv4ManyTile;
+  const float2* stat = reinterpret_cast<const float2*>(a.part_lse);   // (lse, power of two)
   float top = -INFINITY;
 #pragma unroll 8
-  for (int s = p.c0; s <= p.c1; ++s) top = max_nan(top, a.part_lse[p.slot(s) * kKv4ManyTile + row]);
+  for (int s = p.c0; s <= p.c1; ++s) top = max_nan(top, stat[p.slot(s) * kKv4ManyTile + row].x);
   float acc[16], den = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -550,7 +551,8 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
 #pragma unroll 4
     for (int s = p.c0; s <= p.c1; ++s) {
       const size_t slot = p.slot(s);
-      const float f = fast_exp2(a.part_lse[slot * kKv4ManyTile + row] - top);
+      const float2 st = stat[slot * kKv4ManyTile + row];
+      const float f = fast_exp2(st.x - top), g = f * st.y;
       const uint4* src = static_cast<const uint4*>(a.part_o) +
                          (slot * (DH / kPer) + (size_t)chunk * (8 / kPer)) * kKv4ManyTile + row;
       den += f;
@@ -561,10 +563,10 @@ __global__ void __launch_bounds__(kMergeRows* DH / 16) kv4_merge_many_kernel(Kv4
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (kPer == 4) {
-            acc[4 * u + e] += f * __uint_as_float(w[e]);
+            acc[4 * u + e] += g * __uint_as_float(w[e]);
           } else {
-            acc[8 * u + 2 * e] += f * Half<__half>::lo(w[e]);
-            acc[8 * u + 2 * e + 1] += f * Half<__half>::hi(w[e]);
+            acc[8 * u + 2 * e] += g * Half<__half>::lo(w[e]);
+            acc[8 * u + 2 * e + 1] += g * Half<__half>::hi(w[e]);
           }
         }
       }

@@ -54,7 +54,7 @@ struct ManySmem {
   static constexpr uint32_t kQ = 128u * DH * 2u;       // a Q tile
   static constexpr uint32_t kTile = 64u * DH * 2u;     // a K or V tile
   static constexpr size_t kBytes =
-      1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 1024 + 4 * kMaxManyCluster;
+      1024 + 2 * kQ + kRing * kTile + kRaw * Kv4<DH>::kBytes + 640 + 8 * (256 + kMaxManyCluster);
   static_assert(kBytes <= 232448, "shared memory budget");
   static_assert(kRing * kTile + kRaw * Kv4<DH>::kBytes >= (256u + kMaxManyCluster - 1) * DH * 4u,
                 "the rings hold the rows in fp32 that a cluster's CTA joins: of each of n, 1/n of 256, rounded up");
@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   uint8_t* kv_s = q_s + 2 * C::kQ;
   uint8_t* raw_s = kv_s + kRing * C::kTile;
   ManyBars* bars = reinterpret_cast<ManyBars*>(raw_s + kRaw * F::kBytes);
-  float* lse_s = reinterpret_cast<float*>(raw_s + kRaw * F::kBytes + 640);   // a cluster's CTA: its rows' lse
+  // a cluster's CTA: its rows' lse and powers of two
+  float2* stat_s = reinterpret_cast<float2*>(raw_s + kRaw * F::kBytes + 640);
   static_assert(sizeof(ManyBars) <= 640, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = c.head + KV4_WORD_WAIT;
@@ -657,10 +658,28 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       const float lse2 = some ? m_used + kManyShift + log2f(l * (1.f / (1 << kManyShift))) : -INFINITY;
       T* dst = static_cast<T*>(a.out) + pc.seq * a.o_seq + j * a.o_row + h * a.o_head;
       const size_t at = (size_t)pc.slot * kKv4ManyTile + x * 128 + r;
-      // A part for a bf16 output in fp16: half the bytes of fp32, and 2^-11 of a mean of |v| <= 61440 at most; for an
-      // fp16 output, whose own rounding that is, in fp32.  16-byte chunks of the tile's rows lie side by side, so
-      // that a warp's stores and the merge's loads are contiguous
+      // A part for a bf16 output in fp16: half the bytes of fp32.  A power of two brings the row's largest magnitude up
+      // to 2^14 .. 2^15 (a mean of |v| <= 61440 is never above fp16's range), so a value is off by 2^-11 of itself at
+      // most, or by 2^-39 of that largest one.  For an fp16 output, whose own rounding that is, in fp32.  16-byte chunks
+      // of the tile's rows lie side by side, so that a warp's stores and the merge's loads are contiguous
       constexpr int kPer = kPartPer<T>;   // channels of a chunk
+      const bool joined = (Cluster && unit.n > 1) || !pc.whole;
+      float factor = inv, up = 1.f;
+      if (kPer == 8 && joined) {
+        float most = 0.f;
+#pragma unroll 1
+        for (int cb = 0; cb < DH; cb += 32) {
+          float o[32];
+          tmem_ld32(t_o + cb, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) most = max3(most, fabsf(o[e]), fabsf(o[e + 1]));
+        }
+        float down;
+        row_powers(some ? most * inv : 0.f, down, up);
+        up = fminf(up, 1.f);
+        factor = inv * fmaxf(down, 1.f);
+      }
       auto chunk_of = [](const float(&o)[32], int e) {
         if constexpr (kPer == 4)
           return make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
@@ -677,10 +696,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         const int per = (pc.nr + unit.n - 1) / unit.n, owner = min((x * 128 + r) / per, unit.n - 1);
         const int place = unit.rank * per + x * 128 + r - owner * per;
         const uint32_t to = dsmem_map(smem_u32(kv_s) + place * (16 * DH / kPer), owner);
-        const uint32_t to_lse = dsmem_map(smem_u32(lse_s) + 4 * place, owner);
+        const uint32_t to_stat = dsmem_map(smem_u32(stat_s + place), owner);
         cluster_sync();   // the others' rings are free once all their products are complete
         met = true;
-        if (valid) dsmem_st_f1(to_lse, lse2);
+        if (valid) dsmem_st_f2(to_stat, make_float2(lse2, up));
         constexpr int kLanes = DH / 8, kRows = 32 / kLanes;   // the Q tile holds dh / 8 chunks of a row
 #pragma unroll
         for (int half = 0; half < 8 / kPer; ++half) {
@@ -690,7 +709,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
             tmem_ld32(t_o + half * (DH / 2) + cb, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
+            for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * factor : 0.f;
 #pragma unroll
             for (int e = 0; e < 32; e += kPer) *q_chunk(lane, (cb + e) / kPer) = chunk_of(o, e);
           }
@@ -710,7 +729,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           tmem_ld32(t_o + cb, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * inv : 0.f;
+          for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * factor : 0.f;
           if (valid && ok) {
             if (pc.whole) {
 #pragma unroll
@@ -726,7 +745,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         }
         if (valid && ok) {
           if (!pc.whole)
-            a.part_lse[at] = lse2;
+            reinterpret_cast<float2*>(a.part_lse)[at] = make_float2(lse2, up);
           else if (a.lse)
             a.lse[((size_t)pc.seq * a.rows + j) * a.n_q + h] = lse2 * 0.6931471805599453f;
         }
@@ -753,31 +772,32 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
     constexpr int kPer = kPartPer<T>, kChunks = DH / kPer;
     for (int i = threadIdx.x; i < mine * kChunks; i += kManyThreads) {
       const int at = i / kChunks, chunk = i % kChunks;
-      float le[kMaxManyCluster], top = -INFINITY;
+      float2 st[kMaxManyCluster];
+      float top = -INFINITY;
       uint4 v[kMaxManyCluster];
 #pragma unroll
       for (int k = 0; k < kMaxManyCluster; ++k) {   // (all loads before the first use)
-        le[k] = k < n ? lse_s[k * per + at] : -INFINITY;
+        st[k] = k < n ? stat_s[k * per + at] : make_float2(-INFINITY, 1.f);
         v[k] = k < n ? reinterpret_cast<const uint4*>(kv_s)[(k * per + at) * kChunks + chunk] : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int k = 0; k < kMaxManyCluster; ++k) top = max_nan(top, le[k]);
+      for (int k = 0; k < kMaxManyCluster; ++k) top = max_nan(top, st[k].x);
       float acc[kPer], den = 0.f;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
       if (top != -INFINITY) {
 #pragma unroll
         for (int k = 0; k < kMaxManyCluster; ++k) {
-          const float f = fast_exp2(le[k] - top);
+          const float f = fast_exp2(st[k].x - top), g = f * st[k].y;
           const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
           den += f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (kPer == 4) {
-              acc[e] += f * __uint_as_float(w[e]);
+              acc[e] += g * __uint_as_float(w[e]);
             } else {
-              acc[2 * e] += f * Half<__half>::lo(w[e]);
-              acc[2 * e + 1] += f * Half<__half>::hi(w[e]);
+              acc[2 * e] += g * Half<__half>::lo(w[e]);
+              acc[2 * e + 1] += g * Half<__half>::hi(w[e]);
             }
           }
         }

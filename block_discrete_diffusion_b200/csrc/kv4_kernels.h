@@ -61,7 +61,8 @@ struct Kv4Attn {
   void* line;              // header of the division: 16 bytes and n_seq words of 8 bytes
   void* part_o;            // normalised; few rows: fp32 [2 n_ctas][tile][dh]; many: 16-byte chunks of fp16, or of
                            // fp32 for an fp16 output, [2 n_ctas][chunk][tile]
-  float* part_lse;         // [2 n_ctas][rows of a tile], base 2
+  float* part_lse;         // [2 n_ctas][rows of a tile], base 2; many: pairs of it and the power of two by which the
+                           // row's values in part_o are to be multiplied
 };
 
 // Few rows of a KV head (single tokens): tiles of 8 rows, steps of one page, mma.sync on fragments dequantised in

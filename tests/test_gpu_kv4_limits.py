@@ -91,6 +91,24 @@ def test_a_long_tail_behind_one_dominant_key(T, table, dh, dtype, gap, at):
     check_tails(c, q, *run(c, q, scale), scale)
 
 
+@pytest.mark.parametrize("T,table", FORMS + [(200, None), (200, 3000)])
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("power", [-40, -17, -14, -8, 13, "blocks"])
+def test_values_of_any_magnitude(T, table, dh, power):
+    """Outputs in bf16 keep their bits whatever the values' magnitude is, also where rows are joined from parts; values of one row
+    whose blocks of channels are of different magnitudes too."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    k, v = (torch.randn((900, 2, dh), generator=g, device="cuda") for _ in range(2))
+    if power == "blocks":
+        v *= torch.exp2(torch.arange(dh // 16, device="cuda") % 5 * 4.0 - 12).repeat_interleave(16)
+    else:
+        v *= 2.0 ** power
+    q = torch.randn((1, T, 4, dh), generator=g, device="cuda").to(BF16)
+    c = cache_of(k.to(BF16), v.to(BF16), table)
+    scale = float(np.float32(dh ** -0.5))
+    check_tails(c, q, *run(c, q, scale), scale)
+
+
 @pytest.mark.parametrize("T,table", FORMS)
 @pytest.mark.parametrize("dh,dtype", [(64, FP16), (128, BF16)])
 @pytest.mark.parametrize("power", [10, 17, 18, 20, 22, 24, 26, 27, 28, 30, 40, 100])

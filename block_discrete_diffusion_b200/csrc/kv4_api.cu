@@ -295,11 +295,12 @@ DG_API dg_status dg_kv4_error(const dg_kv4_cache* c, void* stream, int* h_code) 
   int32_t w[4] = {0, 0, 0, 0};
   const Kv4View v = view(c);
   cudaError_t e = cudaMemcpyAsync(w, v.head, sizeof w, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(v.head + KV4_WORD_ERR, 0, 4, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(v.head + KV4_WORD_WAIT, 0, 4, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  // a wait that ran out spoils whole outputs, so it comes first; the other word stays for the next call
+  const int word = w[KV4_WORD_WAIT] ? KV4_WORD_WAIT : KV4_WORD_ERR;
+  if (e == cudaSuccess && w[word]) e = cudaMemsetAsync(v.head + word, 0, 4, s);
   if (e != cudaSuccess) return launched(fn, e);
-  *h_code = w[KV4_WORD_ERR] ? w[KV4_WORD_ERR] : w[KV4_WORD_WAIT];
+  *h_code = w[word];
   if (!*h_code) return DG_OK;
   char why[64];
   snprintf(why, sizeof why, "device-side error code %d", *h_code);

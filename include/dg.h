@@ -375,8 +375,9 @@ dg_status dg_kv4_attend(const dg_kv4_cache *c, int layer, const dg_kv4_attn *a, 
 dg_status dg_store_prefix_kv4(dg_seqs *s, int seq, const dg_kv4_cache *cache, int slot);
 dg_status dg_load_prefix_kv4(dg_seqs *s, int seq, int P, const dg_kv4_cache *cache, int slot);
 
-/* Synchronise the stream and return the first device-side error code recorded in the book since the last call
- * (0 = none); the record is cleared.  Returns DG_ERR_DEVICE if non-zero. */
+/* Synchronise the stream and return a device-side error code recorded in the book (0 = none), and clear it.  A wait that
+ * ran out (4) is recorded apart from the other codes, of which the first since it was cleared is kept, and is returned
+ * first: where both are recorded, the next call returns the other.  Returns DG_ERR_DEVICE if non-zero. */
 dg_status dg_kv4_error(const dg_kv4_cache *c, void *stream, int *h_code);
 
 /* Synchronise the handle's stream and return the first device-side error code recorded since the

@@ -195,6 +195,18 @@ def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):
             c.refs.copy_(refs)
 
 
+def test_both_kinds_of_error_are_told():
+    """A wait that ran out and a count that does not fit, both recorded (here by hand): neither hides the other."""
+    c = make(1, 64, [3])
+    x = torch.zeros((1, 4, 1, 64), device="cuda").to(BF16)
+    c.book[3] = 4
+    dg.dg_kv4_append(c, 0, x, x)                        # four rows of three positions
+    assert [dg.dg_kv4_error(c) for _ in range(3)] == [4, 8, 0]
+    dg.dg_kv4_append(c, 0, x, x)
+    c.book[3] = 4
+    assert [dg.dg_kv4_error(c) for _ in range(3)] == [4, 8, 0]
+
+
 # ---------------------------------------------------------------------------------------------
 # a sequence set's prefixes
 # ---------------------------------------------------------------------------------------------

@@ -35,6 +35,9 @@ const char* shape_error(const dg_kv4_cache* c) {
   if (c->n_pages > kMaxPages || c->max_pages > kMaxPages) return "n_pages and max_pages must be at most 2^24";
   if ((long long)c->n_seq * c->max_pages >= 1ll << 30) return "n_seq * max_pages must be below 2^30";
   if ((long long)c->n_seq * c->n_kv > 65535) return "n_seq * n_kv must be at most 65535";
+  // (n_pages * n_kv * 72 * d_head is below 2^54)
+  if ((1ll << 54) / c->n_layers < (long long)c->n_pages * c->n_kv * 72 * c->d_head)
+    return "the pool must be at most 2^54 bytes";
   return nullptr;
 }
 

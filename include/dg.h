@@ -288,7 +288,7 @@ dg_status dg_head_sample_error(void *ws, void *stream, int *h_code);
 #define DG_KV4_PAGE 64   /* positions of a page */
 
 /* d_head 64 or 128; n_seq <= 4096, n_pages and max_pages (of one sequence) <= 2^24, n_seq * max_pages < 2^30,
- * n_seq * n_kv <= 65535.  Buffers 16-byte aligned, of at least dg_kv4_pool_bytes / dg_kv4_book_bytes. */
+ * n_seq * n_kv <= 65535, the pool at most 2^54 bytes.  Buffers 16-byte aligned, of at least dg_kv4_pool_bytes / dg_kv4_book_bytes. */
 typedef struct {
   int n_layers, n_kv, d_head, n_pages, n_seq, max_pages;
   void *d_pool;

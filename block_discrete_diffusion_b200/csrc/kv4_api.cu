@@ -92,6 +92,9 @@ int current_sms() {
   return n;
 }
 
+// Whether some of the n elements of a dimension, d_head channels each, lie on one another: as outputs they would race.
+bool overlap(long long n, int64_t stride, int d_head) { return n > 1 && stride < d_head && -stride < d_head; }
+
 // How a call's work is divided: the form, and the CTAs among which it goes.
 struct Plan {
   bool few;
@@ -152,7 +155,7 @@ Plan plan_of(const dg_kv4_cache* c, int n_q, int rows) {
   return p;
 }
 
-dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_kv4_rows* r) {
+dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_kv4_rows* r, bool out) {
   const dg_status st = check_cache(fn, c);
   if (st != DG_OK) return st;
   if (!r || !aligned16(r->k) || !aligned16(r->v)) return bad(fn, "k and v must be 16-byte aligned device buffers");
@@ -161,6 +164,10 @@ dg_status check_rows(const char* fn, const dg_kv4_cache* c, int layer, const dg_
   if (r->rows <= 0) return bad(fn, "rows must be positive");
   if ((r->k_seq | r->k_row | r->k_head | r->v_seq | r->v_row | r->v_head) & 7)
     return bad(fn, "strides must be multiples of 8 elements");
+  const int dh = c->d_head;
+  if (out && (overlap(c->n_seq, r->k_seq, dh) || overlap(r->rows, r->k_row, dh) || overlap(c->n_kv, r->k_head, dh) ||
+              overlap(c->n_seq, r->v_seq, dh) || overlap(r->rows, r->v_row, dh) || overlap(c->n_kv, r->v_head, dh)))
+    return bad(fn, "rows read out must not overlap");
   return DG_OK;
 }
 
@@ -223,14 +230,14 @@ DG_API dg_status dg_kv4_compact(const dg_kv4_cache* c, void* stream) {
 
 DG_API dg_status dg_kv4_append(const dg_kv4_cache* c, int layer, const dg_kv4_rows* r, void* stream) {
   const char* fn = "dg_kv4_append";
-  const dg_status st = check_rows(fn, c, layer, r);
+  const dg_status st = check_rows(fn, c, layer, r, false);
   if (st != DG_OK) return st;
   return launched(fn, kv4_rows(view(c), layer, rows_of(r), true, static_cast<cudaStream_t>(stream)));
 }
 
 DG_API dg_status dg_kv4_read(const dg_kv4_cache* c, int layer, const dg_kv4_rows* r, void* stream) {
   const char* fn = "dg_kv4_read";
-  const dg_status st = check_rows(fn, c, layer, r);
+  const dg_status st = check_rows(fn, c, layer, r, true);
   if (st != DG_OK) return st;
   return launched(fn, kv4_rows(view(c), layer, rows_of(r), false, static_cast<cudaStream_t>(stream)));
 }
@@ -254,6 +261,9 @@ DG_API dg_status dg_kv4_attend(const dg_kv4_cache* c, int layer, const dg_kv4_at
   if (!(a->scale > 0.f) || !isfinite(a->scale)) return bad(fn, "scale must be positive and finite");
   if ((a->q_seq | a->q_row | a->q_head | a->o_seq | a->o_row | a->o_head) & 7)
     return bad(fn, "strides must be multiples of 8 elements");
+  if (overlap(c->n_seq, a->o_seq, c->d_head) || overlap(a->rows, a->o_row, c->d_head) ||
+      overlap(a->n_q, a->o_head, c->d_head))
+    return bad(fn, "rows of out must not overlap");
   const Plan p = plan_of(c, a->n_q, a->rows);
   if (!ws || ws_bytes < p.bytes(c) + kWorkspaceSlack) return bad(fn, "workspace too small", DG_ERR_CAPACITY);
   Kv4Attn k{};

@@ -336,7 +336,8 @@ typedef struct {
 /* Quantise the rows into the sequences' last positions of one layer (dg_kv4_extend made room for them).  A sequence
  * of which the rows would meet a page with other owners is not written, its other pages neither. */
 dg_status dg_kv4_append(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);
-/* The values that the sequences' last positions of one layer stand for (exact in both types). */
+/* The values that the sequences' last positions of one layer stand for (exact in both types).  The rows must not overlap:
+ * a stride below d_head where there is more than one is refused. */
 dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, void *stream);
 
 /* Attention of n = d_rows[s] (null: rows) query rows of every sequence over its cached positions:
@@ -344,11 +345,12 @@ dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, vo
  * cache); causal = 1: row j is position len - n + j and sees itself and what comes before (a prompt chunk,
  * a single token).  A row that sees nothing is 0 with lse -inf.  Query head h reads KV head h / (n_q / n_kv).
  * Element (s, j, h, c) of q lies at q_seq * s + q_row * j + q_head * h + c elements (strides multiples of 8, rows
- * 16-byte aligned), out likewise; both of type dtype; out may be q.  lse (nullable): fp32 [n_seq][rows][n_q], the natural
- * logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The
- * work is divided among the SMs on the device, by the lengths that it finds there.  NaN and infinities: stale
- * contents behind a sequence's end never matter; a NaN among its cached values reaches every row of the call that
- * reads that page, also rows that the causal mask keeps from that position. */
+ * 16-byte aligned), out likewise (rows of out must not overlap: a stride below d_head where there is more than one is
+ * refused); both of type dtype; out may be q, with the same strides.  lse (nullable): fp32 [n_seq][rows][n_q], the
+ * natural logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The work is divided
+ * among the SMs on the device, by the lengths that it finds there.  NaN and infinities: stale contents behind a
+ * sequence's end never matter; a NaN among its cached values reaches every row of the call that reads that page, also
+ * rows that the causal mask keeps from that position. */
 typedef struct {
   const void *q;
   void *out;

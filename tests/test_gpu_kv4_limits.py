@@ -195,6 +195,21 @@ def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):
             c.refs.copy_(refs)
 
 
+def test_expanded_outputs_are_refused():
+    c = make(2, 64, [5, 6])
+    x = torch.zeros((2, 3, 2, 64), device="cuda").to(BF16)
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 2, 3), dtype=torch.uint8, device="cuda")
+    for wide in (x[:1].expand(2, 3, 2, 64), x[:, :1].expand(2, 3, 2, 64), x[:, :, :1].expand(2, 3, 2, 64)):
+        for call in (lambda: dg.dg_kv4_attend(c, 0, x, wide, ws), lambda: dg.dg_kv4_read(c, 0, wide, x.clone()),
+                     lambda: dg.dg_kv4_read(c, 0, x.clone(), wide)):
+            with pytest.raises(dg.DGError):
+                call()
+        dg.dg_kv4_append(c, 0, wide, x)                 # what is read may be broadcast
+        a = c.pool.clone()
+        dg.dg_kv4_append(c, 0, wide.contiguous(), x)
+        assert torch.equal(a, c.pool)
+
+
 def test_both_kinds_of_error_are_told():
     """A wait that ran out and a count that does not fit, both recorded (here by hand): neither hides the other."""
     c = make(1, 64, [3])

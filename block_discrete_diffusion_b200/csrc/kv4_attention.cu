@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
           }
         }
       }
+      if (!here) m[0] = m[1] = NAN;   // a page that is none: the rows that it belongs to are not to be taken for whole
       __syncwarp();   // every lane has read the stage
       if (i + kFewStages < n_mine) {
         const bool again = fetch(i + kFewStages);

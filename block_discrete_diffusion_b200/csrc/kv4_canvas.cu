@@ -74,7 +74,7 @@ struct ManyBars {
   Task task[kTasks];
   uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2][2];   // by tile, by S buffer
   uint64_t kv_full[kRing], kv_empty[kRing], raw_full[kRaw], raw_empty[kRaw];
-  int raw_there[kRaw];   // 0: the page is behind the sequence's end (or not one): its values count as zeros
+  int raw_there[kRaw];   // 0: the table names no page here: its scores are NaN, and so are the rows that see it
   uint32_t tmem;
 };
 
@@ -247,9 +247,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
             }
           }
         }
-        // a page that is not there: code 0 at scale 0 for all
+        // a page that is not there: K is code 0 at scale NaN, V any code at scale 0
         if (!there) {
-          ks = vs[0] = vs[1] = 0;
+          ks = 0xffffffffu;
+          vs[0] = vs[1] = 0;
 #pragma unroll
           for (int jh = 0; jh < F::kH; ++jh) k[jh] = make_uint4(0, 0, 0, 0);
         }

@@ -280,8 +280,8 @@ dg_status dg_head_sample_error(void *ws, void *stream, int *h_code);
  * V's codes, K's scales and V's scales in the order of the tensor-core fragments that read them.
  *
  * Calls on one cache share its book, so they must be ordered (one stream, or events).  Checks that need device
- * data happen in the kernels: a call that fails them changes nothing (rows of the sequence at fault are
- * skipped) and records a code for dg_kv4_error: 5 an index out of range, a page written that has other
+ * data happen in the kernels: a call that fails them changes nothing (of calls on rows, those of the sequence at fault
+ * are skipped; see dg_kv4_attend for pages) and records a code for dg_kv4_error: 5 an index out of range, a page written that has other
  * owners, or a sequence named twice; 7 too few free pages; 8 a count that does not fit its sequence; 4 a wait inside a
  * kernel ran out (its outputs are not to be used).
  * ------------------------------------------------------------------------------------------------ */
@@ -348,7 +348,8 @@ dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, vo
  * 16-byte aligned), out likewise (rows of out must not overlap: a stride below d_head where there is more than one is
  * refused); both of type dtype; out may be q, with the same strides.  lse (nullable): fp32 [n_seq][rows][n_q], the
  * natural logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The work is divided
- * among the SMs on the device, by the lengths that it finds there.  NaN and infinities: stale contents behind a
+ * among the SMs on the device, by the lengths that it finds there.  Rows of a sequence that would read a page out of
+ * range (code 5) are NaN.  NaN and infinities: stale contents behind a
  * sequence's end never matter; a NaN among its cached values reaches every row of the call that reads that page, also
  * rows that the causal mask keeps from that position. */
 typedef struct {

@@ -222,6 +222,31 @@ def test_both_kinds_of_error_are_told():
     assert [dg.dg_kv4_error(c) for _ in range(3)] == [4, 8, 0]
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T,table", FORMS)
+@pytest.mark.parametrize("page", [-1, 99])
+@pytest.mark.parametrize("at", [0, 3, 10])
+def test_rows_that_would_read_a_page_that_is_none_are_nan(T, table, dtype, page, at):
+    """... beside other sequences' rows, which are what they are without it, and rows that end before it."""
+    c = make(2, 128, [700, 700, 300], max_pages=table)
+    q = torch.randn((3, T, 4, 128), device="cuda").to(dtype)
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 4, T), dtype=torch.uint8, device="cuda")
+    outs = []
+    for bad in (False, True):
+        if bad:
+            c.table[1, at] = page
+        out, lse = torch.full_like(q, 3), torch.full(q.shape[:3], 7.0, device="cuda")
+        dg.dg_kv4_attend(c, 0, q, out, ws, lse=lse)
+        assert dg.dg_kv4_error(c) == (5 if bad else 0)
+        outs.append((out, lse))
+    for x, y in zip(*outs):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[2], y[2]) and bool(x.isfinite().all())
+        assert bool(y[1].isnan().all())
+    c.lens[1] = 64 * at                                 # a sequence that ends before that entry does not read it
+    dg.dg_kv4_attend(c, 0, q, outs[0][0], ws)
+    assert dg.dg_kv4_error(c) == 0 and bool(outs[0][0].isfinite().all())
+
+
 # ---------------------------------------------------------------------------------------------
 # a sequence set's prefixes
 # ---------------------------------------------------------------------------------------------

@@ -371,21 +371,21 @@ __device__ int block_scan(int v, int* total) {
 // What a sequence needs to grow by `count`: pages it has, whether it copies its last one, pages to take.
 struct Growth {
   int have, copy, need, last;
-  bool bad;
+  int bad;   // 0, or the code of what does not fit
 };
 __device__ Growth growth(const Kv4View& c, const int32_t* counts, int seq) {
-  Growth g{0, 0, 0, -1, false};
+  Growth g{0, 0, 0, -1, 0};
   const int len = c.lens[seq], n = counts[seq];
   const long long now = (long long)len + n;
   if (n < 0 || len < 0 || now > (long long)c.max_pages * kPage) {
-    g.bad = true;
+    g.bad = DEV_ERR_BAD_COUNT;
     return g;
   }
   g.have = pages_of(len);
   if (n > 0 && len % kPage) {
     g.last = c.table[(size_t)seq * c.max_pages + g.have - 1];
     if (g.last < 0 || g.last >= c.n_pages) {
-      g.bad = true;
+      g.bad = DEV_ERR_BAD_INDEX;
       return g;
     }
     g.copy = c.refs[g.last] > 1;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kBookThreads) kv4_extend_kernel(Kv4View c, con
   int mine = 0;
   for (int s = threadIdx.x * per; s < min(c.n_seq, (int)(threadIdx.x + 1) * per); ++s) {
     const Growth g = growth(c, counts, s);
-    if (g.bad) bad = 1;
+    if (g.bad) atomicMax(&bad, g.bad);
     mine += g.need;
   }
   int total;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kBookThreads) kv4_extend_kernel(Kv4View c, con
   __syncthreads();
   if (bad) {
     if (threadIdx.x == 0) {
-      report_error(c.head, DEV_ERR_BAD_COUNT);
+      report_error(c.head, bad);
       c.head[KV4_WORD_MOVES] = 0;
     }
     return;

@@ -195,6 +195,21 @@ def test_rows_move_whole_or_not_at_all(dh, dtype, n_pages):
             c.refs.copy_(refs)
 
 
+@pytest.mark.parametrize("page", [-1, 99])
+def test_growth_behind_a_page_that_is_none(page):
+    """The last page's table entry is out of range: nothing grows, and the code is that of an index (a count that does not fit, of
+    another sequence, comes before it)."""
+    c = make(1, 64, [70, 5, 64])
+    c.table[0, 1] = page
+    book, pool = c.book.clone(), c.pool.clone()
+    for counts, code in (([1, 0, 0], 5), ([1, 2, 0], 5), ([1, -1, 0], 8), ([1, 0, 1 << 20], 8)):
+        dg.dg_kv4_extend(c, dev(counts))
+        assert dg.dg_kv4_error(c) == code
+        assert torch.equal(c.book[16:], book[16:]) and torch.equal(c.pool, pool)
+    dg.dg_kv4_extend(c, dev([0, 2, 0]))                 # what does not grow is not looked at
+    assert dg.dg_kv4_error(c) == 0 and c.lens.tolist() == [70, 7, 64]
+
+
 def test_expanded_outputs_are_refused():
     c = make(2, 64, [5, 6])
     x = torch.zeros((2, 3, 2, 64), device="cuda").to(BF16)

@@ -161,10 +161,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
     float o[NJ][4];               // O^T: channels DH/8 g + 2 j + {0, 1}, rows 2t, 2t + 1
 #pragma unroll
     for (int j = 0; j < NJ; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    for (int i = 0; i < n_mine; ++i) {
+    int i = 0;
+    for (; i < n_mine; ++i) {
       const int st = i % kFewStages;
-      ok = ok && mbar_wait(&sm.full[warp][st], (phase >> st) & 1, c.head + KV4_WORD_WAIT, DEV_ERR_TIMEOUT_ATTN);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = warp_wait(&sm.full[warp][st], (phase >> st) & 1, c.head + KV4_WORD_WAIT);
+      if (!ok) break;
       phase ^= 1 << st;
       const bool here = (present >> st) & 1;
       const int base = (p0 + warp + i * kFewWarps) * kPage;
@@ -292,9 +293,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, kv4_few_ctas(DH))
       }
     }
     // (a wait that ran out: the error word tells; the copies still in flight land in this CTA's memory, so wait on)
-    if (!ok)
-      for (int s = 0; s < kFewStages; ++s)
-        for (int k = 0; k < 2; ++k) mbar_wait(&sm.full[warp][s], k, nullptr, 0);
+    for (int k = i; k < n_mine && k < i + kFewStages; ++k)
+      mbar_wait(&sm.full[warp][k % kFewStages], (phase >> (k % kFewStages)) & 1, nullptr, 0);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);

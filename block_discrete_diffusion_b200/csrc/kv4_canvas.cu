@@ -75,7 +75,9 @@ struct ManyBars {
   uint64_t q_full[2], s_full[2][2], p_ready[2][2], pv_done[2][2];   // by tile, by S buffer
   uint64_t kv_full[kRing], kv_empty[kRing], raw_full[kRaw], raw_empty[kRaw];
   int raw_there[kRaw];   // 0: the table names no page here: its scores are NaN, and so are the rows that see it
-  uint32_t tmem;
+  uint64_t drained[2];    // a tile's products, after a wait that ran out
+  uint32_t tmem, copies;  // (of blocks, started)
+  int lost;               // a wait of this CTA ran out
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -142,7 +144,10 @@ struct Tasks {
   uint32_t i = 0;
   __device__ __forceinline__ bool next(Task& t) {   // whole warp
     const int k = i % kTasks;
-    if (!warp_wait(&bars->task_full[k], (i / kTasks) & 1, err)) return false;
+    if (!warp_wait(&bars->task_full[k], (i / kTasks) & 1, err)) {
+      bars->lost = 1;
+      return false;
+    }
     t = bars->task[k];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->task_empty[k]);
@@ -171,6 +176,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->q_full[x], 4);
+      mbar_init(&bars->drained[x], 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars->s_full[x][b], 1);
         mbar_init(&bars->pv_done[x][b], 1);
@@ -190,6 +196,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       mbar_init(&bars->task_empty[k], kTaskReaders);
     }
     fence_mbar_init();
+    bars->lost = 0;
   }
   if (warp == 12) tmem_alloc(&bars->tmem, 512);   // tile x: S [128 x, +64) and [128 x + 64, +64), O [256 + 128 x, ..)
   tc_fence_before();
@@ -337,6 +344,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         }
       }
     }
+    if (!ok) bars->lost = 1;
     if constexpr (Cluster) {
       __syncwarp();
       if (unit.n > 1) cluster_sync();
@@ -379,7 +387,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         for (uint32_t i = 0;; ++i) {
           const int k = i % kTasks;
           const bool more = stretch.next(p);
-          if (!warp_wait(&bars->task_empty[k], ((i / kTasks) & 1) ^ 1, err)) break;
+          ok = warp_wait(&bars->task_empty[k], ((i / kTasks) & 1) ^ 1, err);
+          if (!ok) break;
           if (lane == 0) {
             bars->task[k] = more ? task_of(p) : none;
             mbar_arrive(&bars->task_full[k]);
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         const int32_t* table = c.table + (size_t)pc.seq * c.max_pages;
         const uint8_t* plane = c.pool + ((size_t)layer * c.n_pages * c.n_kv + pc.head) * F::kBytes;
         int ids = -1;   // 32 pages' ids at a time, one a lane
-        for (int i = 0; i < pc.steps && ok; ++i, ++page) {
+        for (int i = 0; i < pc.steps; ++i, ++page) {
           if ((i & 31) == 0) {
             const bool wanted = i + lane < pc.steps;   // (the steps end at the last page that a row sees)
             ids = wanted ? table[pc.s0 + i + lane] : -1;
@@ -407,7 +416,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           const int id = __shfl_sync(0xffffffffu, ids, i & 31);
           const uint32_t slot = page % kRaw;
           ok = warp_wait(&bars->raw_empty[slot], ((page / kRaw) & 1) ^ 1, err);
-          if (ok && lane == 0) {
+          if (!ok) break;
+          if (lane == 0) {
             bars->raw_there[slot] = id >= 0;
             if (id >= 0) {
               mbar_arrive_expect_tx(&bars->raw_full[slot], F::kBytes);
@@ -420,9 +430,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
           __syncwarp();
         }
       }
-      // (after a wait that ran out: copies still in flight land in this CTA's memory)
-      if (!ok)
-        for (int k = 0; k < 2 * kRaw; ++k) mbar_wait(&bars->raw_full[k / 2], k & 1, nullptr, 0);
+      bars->copies = page;
     } else {
       // ------------------------------ products of tile x ------------------------------
       // (the whole warp waits, lane 0 issues)
@@ -492,6 +500,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
         item += 2 * steps;
       }
     }
+    if (!ok) bars->lost = 1;
     __syncwarp();
     if constexpr (Cluster) {
       if (unit.n > 1) cluster_sync();
@@ -753,6 +762,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
       }
       tc_fence_before();   // O is read before the next piece's products overwrite it (they wait for p_ready)
     }
+    if (!ok) bars->lost = 1;
     // (a cluster's CTA goes on with all its warps: everyone back to the registers of the launch)
     if constexpr (Cluster) {
       cp_async_wait_all();
@@ -763,6 +773,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) kv4_attend_many_kernel(Kv4Vie
   }
   tc_fence_before();
   __syncthreads();
+  if (bars->lost) {
+    // Nobody has waited for what may still be under way: copies into this CTA's memory, products that read it and write
+    // its tensor memory
+    if (warp == 14)
+      for (uint32_t n = bars->copies, k = 1; k <= kRaw && k <= n; ++k)
+        mbar_wait(&bars->raw_full[(n - k) % kRaw], ((n - k) / kRaw) & 1, nullptr, 0);
+    if ((warp == 12 || warp == 15) && lane == 0) {
+      uint64_t* bar = &bars->drained[warp == 12 ? 0 : 1];
+      umma_commit(bar);
+      mbar_wait(bar, 0, nullptr, 0);
+    }
+    __syncthreads();
+  }
   if (warp == 12) tmem_dealloc(tmem, 512);
   if (Cluster && unit.n > 1) {
     // every CTA of the cluster has its share of the unit's rows from all of them, and joins it, a thread for a

@@ -281,9 +281,10 @@ dg_status dg_head_sample_error(void *ws, void *stream, int *h_code);
  *
  * Calls on one cache share its book, so they must be ordered (one stream, or events).  Checks that need device
  * data happen in the kernels: a call that fails them changes nothing (of calls on rows, those of the sequence at fault
- * are skipped; see dg_kv4_attend for pages) and records a code for dg_kv4_error: 5 an index out of range, a page written that has other
- * owners, or a sequence named twice; 7 too few free pages; 8 a count that does not fit its sequence; 4 a wait inside a
- * kernel ran out (its outputs are not to be used).
+ * are skipped; see dg_kv4_attend for pages) and records a code for dg_kv4_error: 5 an index out of range, a page
+ * written that has other owners, or a sequence named twice; 7 too few free pages; 8 a count that does not fit its
+ * sequence; 4 a wait inside a kernel ran out (its outputs are not to be used, nor those of attention calls behind it
+ * until dg_kv4_error has told).
  * ------------------------------------------------------------------------------------------------ */
 #define DG_KV4_PAGE 64   /* positions of a page */
 

@@ -262,6 +262,24 @@ def test_rows_that_would_read_a_page_that_is_none_are_nan(T, table, dtype, page,
     assert dg.dg_kv4_error(c) == 0 and bool(outs[0][0].isfinite().all())
 
 
+@pytest.mark.parametrize("T,table", FORMS)
+def test_calls_after_a_wait_ran_out(T, table):
+    """Once the book says so (here by hand), waits that do not end at once are given up. The calls come to their end all the same,
+    the code is told once, and the calls behind that are right."""
+    c = make(8, 128, [3000, 700], max_pages=table)
+    q = torch.randn((2, T, 16, 128), device="cuda").to(BF16)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(dg.dg_kv4_attend_workspace_bytes(c, 16, T), dtype=torch.uint8, device="cuda")
+    dg.dg_kv4_attend(c, 0, q, want, ws)
+    for _ in range(3):
+        c.book[3] = 4
+        for _ in range(5):
+            dg.dg_kv4_attend(c, 0, q, out, ws)
+        assert dg.dg_kv4_error(c) == 4 and dg.dg_kv4_error(c) == 0
+        dg.dg_kv4_attend(c, 0, q, out, ws)
+        assert dg.dg_kv4_error(c) == 0 and torch.equal(out, want)
+
+
 # ---------------------------------------------------------------------------------------------
 # a sequence set's prefixes
 # ---------------------------------------------------------------------------------------------

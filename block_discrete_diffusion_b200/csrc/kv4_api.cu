@@ -95,7 +95,9 @@ int current_sms() {
 // Whether some of the n elements of a dimension, d_head channels each, lie on one another: as outputs they would race.
 bool overlap(long long n, int64_t stride, int d_head) { return n > 1 && stride < d_head && -stride < d_head; }
 
-// How a call's work is divided: the form, and the CTAs among which it goes.
+// How a call's work is divided: the form, and the CTAs among which it goes.  The host knows no lengths, so where they
+// matter it goes by max_pages, the length that a sequence may have: with a table of 512 pages one token behind 577
+// positions takes 11.0 us instead of 7.6, one canvas behind 2048 24.3 instead of 19.7 (a line and a second launch).
 struct Plan {
   bool few;
   int cluster, n_ctas, min_share;

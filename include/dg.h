@@ -349,8 +349,9 @@ dg_status dg_kv4_read(const dg_kv4_cache *c, int layer, const dg_kv4_rows *r, vo
  * 16-byte aligned), out likewise (rows of out must not overlap: a stride below d_head where there is more than one is
  * refused); both of type dtype; out may be q, with the same strides.  lse (nullable): fp32 [n_seq][rows][n_q], the
  * natural logarithm of sum exp(scale q k).  Rows j >= n of out and lse are left as they were.  The work is divided
- * among the SMs on the device, by the lengths that it finds there.  Rows of a sequence that would read a page out of
- * range (code 5) are NaN.  NaN and infinities: stale contents behind a
+ * among the SMs on the device, by the lengths that it finds there; whether a small call is one launch or two goes by
+ * max_pages, so a table much longer than the lengths costs it 3 to 8 us.  Rows of a sequence that would read a page out
+ * of range (code 5) are NaN.  NaN and infinities: stale contents behind a
  * sequence's end never matter; a NaN among its cached values reaches every row of the call that reads that page, also
  * rows that the causal mask keeps from that position. */
 typedef struct {

@@ -375,8 +375,9 @@ dg_status dg_kv4_attend(const dg_kv4_cache *c, int layer, const dg_kv4_attn *a, 
  * and pages without other owners; dg_load_prefix_kv4 installs the prefix that `slot` holds, of length P, as sequence
  * `seq`'s (replacing its cache content, as dg_load_prefix does).  The cache has the model's layers, KV heads and
  * d_head.  Both run on the handle's stream; a length other than P is recorded in the cache's book (code 8) and moves
- * nothing.  A load waits for the stream once, to see that the slot fits: one that does not leaves the sequence as it was,
- * its length included, and its code (8, or 5 for a page out of range) is what dg_device_error tells next. */
+ * nothing.  A load waits for the stream once, to see that the slot fits (so it is not for capture into a graph): one that
+ * does not leaves the sequence as it was, its length included, and its code (8, or 5 for a page out of range) is what
+ * dg_device_error tells next. */
 dg_status dg_store_prefix_kv4(dg_seqs *s, int seq, const dg_kv4_cache *cache, int slot);
 dg_status dg_load_prefix_kv4(dg_seqs *s, int seq, int P, const dg_kv4_cache *cache, int slot);
 

@@ -30,6 +30,15 @@ def test_canvas_with_fewer_pages_than_its_cluster_has_ctas(lens, causal):
         attend(c, 2, 256, BF16, rows=[130], causal=causal, seed=seed, q_scale=2.0 ** 122, scale=2.0 ** -124)
 
 
+@pytest.mark.parametrize("table", [None, 3000])
+@pytest.mark.parametrize("n_q,n_kv,dh,dtype", [(4, 2, 128, BF16), (2, 2, 64, FP16)])
+def test_whole_prompts(n_q, n_kv, dh, dtype, table):
+    """Causal rows for every position, more than a tile has and more of one sequence than of another; and the last rows of it."""
+    c = make(n_kv, dh, [1300, 517, 64], max_pages=table)
+    attend(c, n_q, 1300, dtype, rows=[1300, 517, 64], causal=True)
+    attend(c, n_q, 1300, dtype, rows=[700, 517, 1], causal=True)
+
+
 # ---------------------------------------------------------------------------------------------
 # attention at the ends of the number ranges
 # ---------------------------------------------------------------------------------------------
